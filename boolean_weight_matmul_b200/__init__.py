@@ -22,6 +22,8 @@ BF16 = 1
 GROUP = 128
 MAX_K = 4
 MAX_BATCH = 16
+DISTILL_MAX_TOP = 512
+DISTILL_MAX_VOCAB = 1 << 21
 GEMV_AUTO = 0
 GEMV_LOOKUP = 1
 GEMV_TENSOR = 2
@@ -48,7 +50,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing; build it with "
                                "`python -m boolean_weight_matmul_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
-        vp, i, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        vp, i, sz, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
         sigs = {
             "mbok_status_string": ([i], ctypes.c_char_p),
             "mbok_layout_version": ([], i),
@@ -73,6 +75,11 @@ def lib() -> ctypes.CDLL:
             "mbok_svid_workspace_bytes": ([i, i], sz),
             "mbok_svid_binarize": ([vp, i, i, i, i, vp, vp, vp, vp, vp, sz, vp], i),
             "mbok_gemv_multi_workspace_bytes": ([i, vp, vp, i], sz),
+            "mbok_gemv_gated_workspace_bytes": ([i, i, i, i, i], sz),
+            "mbok_gemv_gated": ([vp, vp, i, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, sz, vp], i),
+            "mbok_gated_backward": ([vp, vp, vp, i, i, vp, vp, vp, vp], i),
+            "mbok_distill_loss": ([vp, i, i, i, sz, vp, vp, i, f, vp, vp, vp, vp, sz, vp], i),
+            "mbok_distill_backward": ([vp, i, i, i, sz, vp, vp, i, f, vp, vp, vp, vp, sz, vp], i),
             "mbok_gemv_multi": ([i, vp, vp, vp, vp, i, i, vp, i, i, vp, vp, sz, vp], i),
         }
         for name, (args, res) in sigs.items():
@@ -263,6 +270,53 @@ def gemv_svid(packed, s_in, s_out, K, M, N, x, x_dtype, batch, y, workspace, str
     pp, pi, po, px, py, pws = _ptrs(packed, s_in, s_out, x, y, workspace)
     _check(lib().mbok_gemv_svid(pp, pi, po, K, M, N, px, x_dtype, batch, py, pws, ws_bytes, _stream(stream)),
            "mbok_gemv_svid")
+
+
+def _ws_bytes(workspace) -> int:
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
+
+
+def gemv_gated_workspace_bytes(K_gate: int, K_up: int, M: int, N: int, batch: int = 1) -> int:
+    return int(lib().mbok_gemv_gated_workspace_bytes(K_gate, K_up, M, N, batch))
+
+
+def empty_gated_workspace(K_gate: int, K_up: int, M: int, N: int, batch: int = 1, device="cuda") -> torch.Tensor:
+    n = max(gemv_gated_workspace_bytes(K_gate, K_up, M, N, batch), 256)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gemv_gated(packed_gate, alpha_gate, K_gate, packed_up, alpha_up, K_up, M, N, group, x, x_dtype, batch, h, h_dtype,
+               workspace, stream=None) -> None:
+    """Decode step of a gated feed-forward block: h = silu(W_gate x) * (W_up x)
+    for 1..16 vectors, h fp32 or bf16 (see include/mbok.h)."""
+    pg, ag, pu, au, px, ph, pws = _ptrs(packed_gate, alpha_gate, packed_up, alpha_up, x, h, workspace)
+    _check(lib().mbok_gemv_gated(pg, ag, K_gate, pu, au, K_up, M, N, group, px, x_dtype, batch, ph, h_dtype, pws,
+                                 _ws_bytes(workspace), _stream(stream)), "mbok_gemv_gated")
+
+
+def gated_backward(dH, gate, up, T, M, dgate, dup, H=None, stream=None) -> None:
+    """Gradient of the gate: dgate and dup from dH and the two projections;
+    with H given, the gated product again (see include/mbok.h)."""
+    ph, pg, pu, qg, qu, qh = _ptrs(dH, gate, up, dgate, dup, H)
+    _check(lib().mbok_gated_backward(ph, pg, pu, T, M, qg, qu, qh, _stream(stream)), "mbok_gated_backward")
+
+
+def distill_loss(logits, dtype, T, V, ld, teacher, index, top, temperature, weight, loss, lse, dlogits=None,
+                 ld_dlogits=0, stream=None) -> None:
+    """KL loss of the logits against a teacher's top logits, with the
+    log-sum-exp and, if dlogits is given, the gradient (see include/mbok.h)."""
+    pz, pt, pi, pw, pl, pe, pd = _ptrs(logits, teacher, index, weight, loss, lse, dlogits)
+    _check(lib().mbok_distill_loss(pz, dtype, T, V, ld, pt, pi, top, temperature, pw, pl, pe, pd, ld_dlogits,
+                                   _stream(stream)), "mbok_distill_loss")
+
+
+def distill_backward(logits, dtype, T, V, ld, teacher, index, top, temperature, weight, lse, grad, dlogits,
+                     ld_dlogits, stream=None) -> None:
+    """Gradient of distill_loss from its lse and the loss's own gradient
+    `grad` (None for 1; see include/mbok.h)."""
+    pz, pt, pi, pw, pe, pg, pd = _ptrs(logits, teacher, index, weight, lse, grad, dlogits)
+    _check(lib().mbok_distill_backward(pz, dtype, T, V, ld, pt, pi, top, temperature, pw, pe, pg, pd, ld_dlogits,
+                                       _stream(stream)), "mbok_distill_backward")
 
 
 def gemv_noalloc(packed, alpha, K, M, N, group, x, x_dtype, batch, y, stream=None) -> None:

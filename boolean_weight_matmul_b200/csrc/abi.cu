@@ -2,6 +2,7 @@
 // the caller's stream.  Nothing here allocates, synchronises or keeps state
 // beyond cached kernel attributes.
 #include <atomic>
+#include <cmath>
 
 #include "mbok_common.cuh"
 
@@ -34,6 +35,17 @@ cudaError_t launch_gemv(const uint8_t*, const uint16_t*, const Shape&, const voi
 cudaError_t launch_gemv_lut_multi(int, const uint8_t* const*, const uint16_t* const*, const int*, const int*, int,
                                   const void*, bool, float*, void*, cudaStream_t, bool);
 size_t gemv_multi_workspace_bytes(int, const int*, const int*, int);
+
+size_t gemv_gated_workspace_bytes(const Shape&);
+cudaError_t launch_gemv_gated(const uint8_t*, const uint16_t*, const Shape&, const uint8_t*, const uint16_t*,
+                              const Shape&, const void*, bool, int, void*, bool, void*, cudaStream_t, bool);
+unsigned gemv_gated_error_flags();
+cudaError_t launch_gated_backward(const uint16_t*, const uint16_t*, const uint16_t*, size_t, uint16_t*, uint16_t*,
+                                  uint16_t*, cudaStream_t);
+cudaError_t launch_distill_loss(const void*, bool, int, int, size_t, const float*, const int*, int, float,
+                                const float*, float*, float*, void*, size_t, cudaStream_t);
+cudaError_t launch_distill_backward(const void*, bool, int, int, size_t, const float*, const int*, int, float,
+                                    const float*, const float*, const float*, void*, size_t, cudaStream_t);
 
 cudaError_t launch_gemm_tc(const uint8_t*, const uint16_t*, const Shape&, const uint16_t*, int,
                            uint16_t*, bool, cudaStream_t);
@@ -99,6 +111,12 @@ int check_shape(int K, int M, int N) {
   if (M > (1 << 22) || N > (1 << 20)) return MBOK_ERR_SHAPE;
   return MBOK_OK;
 }
+
+constexpr int kMaxTokens = 1 << 23;   // as mbok_gemm
+constexpr int kMaxRows = 1 << 22;     // as check_shape
+
+inline bool is_dtype(int d) { return d == MBOK_F32 || d == MBOK_BF16; }
+inline size_t dtype_bytes(int d) { return d == MBOK_F32 ? 4 : 2; }
 
 inline int from_cuda(cudaError_t e) { return e == cudaSuccess ? MBOK_OK : MBOK_ERR_CUDA; }
 
@@ -289,6 +307,88 @@ int mbok_gemv_multi(int nseg, const uint32_t* const* packed, const uint16_t* con
   return MBOK_OK;
 }
 
+size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int batch) {
+  if (check_shape(K_gate, M, N) != MBOK_OK || check_shape(K_up, M, N) != MBOK_OK) return 0;
+  if (batch != 1) return 0;   // the tensor-core kernel needs none (nor does a bad batch)
+  return gemv_gated_workspace_bytes(make_shape(K_gate, M, N));
+}
+
+int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
+                    const uint16_t* alpha_up, int K_up, int M, int N, int group, const void* x, int x_dtype, int batch,
+                    void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_shape(K_gate, M, N);
+  if (st == MBOK_OK) st = check_shape(K_up, M, N);
+  if (st != MBOK_OK) return st;
+  if (group != MBOK_GROUP) return MBOK_ERR_UNSUPPORTED;
+  if (packed_gate == nullptr || alpha_gate == nullptr || packed_up == nullptr || alpha_up == nullptr ||
+      x == nullptr || h == nullptr)
+    return MBOK_ERR_INVALID_ARG;
+  if (!is_dtype(x_dtype) || !is_dtype(h_dtype)) return MBOK_ERR_INVALID_ARG;
+  if (batch < 1 || batch > MBOK_MAX_BATCH) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(packed_gate, 16) || !aligned(alpha_gate, 16) || !aligned(packed_up, 16) || !aligned(alpha_up, 16) ||
+      !aligned(x, 16) || !aligned(h, dtype_bytes(h_dtype)))
+    return MBOK_ERR_ALIGN;
+  const Shape gate = make_shape(K_gate, M, N), up = make_shape(K_up, M, N);
+  const size_t need = batch == 1 ? gemv_gated_workspace_bytes(gate) : 0;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
+    return MBOK_ERR_WORKSPACE;
+  return from_cuda(launch_gemv_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate, gate,
+                                     reinterpret_cast<const uint8_t*>(packed_up), alpha_up, up, x,
+                                     x_dtype == MBOK_F32, batch, h, h_dtype == MBOK_BF16, workspace,
+                                     as_stream(stream), gemv_weights_static.load(std::memory_order_relaxed)));
+}
+
+int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t* up, int T, int M, uint16_t* dgate,
+                        uint16_t* dup, uint16_t* H, void* stream) {
+  if (T < 1 || T > kMaxTokens || M < 1 || M > kMaxRows) return MBOK_ERR_SHAPE;
+  const size_t n = size_t(T) * size_t(M);
+  if (n > (size_t(1) << 42)) return MBOK_ERR_SHAPE;   // keeps the grid in range
+  if (dH == nullptr || gate == nullptr || up == nullptr || dgate == nullptr || dup == nullptr)
+    return MBOK_ERR_INVALID_ARG;
+  if (!aligned(dH, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(dgate, 16) || !aligned(dup, 16) ||
+      !aligned(H, 16))
+    return MBOK_ERR_ALIGN;
+  return from_cuda(launch_gated_backward(dH, gate, up, n, dgate, dup, H, as_stream(stream)));
+}
+
+// Checks common to the distillation calls.
+static int check_distill(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
+                         const int32_t* index, int top, float temperature) {
+  if (!is_dtype(dtype)) return MBOK_ERR_INVALID_ARG;
+  if (T < 1 || T > kMaxTokens || V < 1 || V > MBOK_DISTILL_MAX_VOCAB || ld < size_t(V)) return MBOK_ERR_SHAPE;
+  if (logits == nullptr || teacher == nullptr || index == nullptr) return MBOK_ERR_INVALID_ARG;
+  if (top < 1 || top > MBOK_DISTILL_MAX_TOP) return MBOK_ERR_INVALID_ARG;
+  if (!(temperature >= 1.f / 1024.f && temperature <= 1024.f)) return MBOK_ERR_INVALID_ARG;   // NaN too
+  if (!aligned(logits, 16) || !aligned(teacher, 4) || !aligned(index, 4)) return MBOK_ERR_ALIGN;
+  return MBOK_OK;
+}
+
+int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
+                      const int32_t* index, int top, float temperature, const float* weight, float* loss, float* lse,
+                      void* dlogits, size_t ld_dlogits, void* stream) {
+  const int st = check_distill(logits, dtype, T, V, ld, teacher, index, top, temperature);
+  if (st != MBOK_OK) return st;
+  if (loss == nullptr || lse == nullptr) return MBOK_ERR_INVALID_ARG;
+  if (dlogits != nullptr && ld_dlogits < size_t(V)) return MBOK_ERR_SHAPE;
+  if (dlogits == logits && ld_dlogits != ld) return MBOK_ERR_SHAPE;   // in place: the same rows
+  if (!aligned(weight, 4) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(dlogits, 16)) return MBOK_ERR_ALIGN;
+  return from_cuda(launch_distill_loss(logits, dtype == MBOK_F32, T, V, ld, teacher, index, top, temperature, weight,
+                                       loss, lse, dlogits, ld_dlogits, as_stream(stream)));
+}
+
+int mbok_distill_backward(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
+                          const int32_t* index, int top, float temperature, const float* weight, const float* lse,
+                          const float* grad, void* dlogits, size_t ld_dlogits, void* stream) {
+  const int st = check_distill(logits, dtype, T, V, ld, teacher, index, top, temperature);
+  if (st != MBOK_OK) return st;
+  if (lse == nullptr || dlogits == nullptr) return MBOK_ERR_INVALID_ARG;
+  if (ld_dlogits < size_t(V)) return MBOK_ERR_SHAPE;
+  if (dlogits == logits && ld_dlogits != ld) return MBOK_ERR_SHAPE;
+  if (!aligned(weight, 4) || !aligned(lse, 4) || !aligned(grad, 4) || !aligned(dlogits, 16)) return MBOK_ERR_ALIGN;
+  return from_cuda(launch_distill_backward(logits, dtype == MBOK_F32, T, V, ld, teacher, index, top, temperature,
+                                           weight, lse, grad, dlogits, ld_dlogits, as_stream(stream)));
+}
+
 int mbok_gemv_set_static_weights(int on) {
   if (on != 0 && on != 1) return MBOK_ERR_INVALID_ARG;
   gemv_weights_static.store(on == 1, std::memory_order_relaxed);
@@ -343,8 +443,9 @@ int mbok_read_device_errors(unsigned* flags) {
   const unsigned g = gemv_lut4_error_flags();
   const unsigned m = gemm_error_flags();
   const unsigned t = gemv_mma_error_flags();
-  if (g == ~0u || m == ~0u || t == ~0u) return MBOK_ERR_CUDA;
-  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | (t ? 4u : 0u);
+  const unsigned d = gemv_gated_error_flags();
+  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u) return MBOK_ERR_CUDA;
+  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u);
   return MBOK_OK;
 }
 

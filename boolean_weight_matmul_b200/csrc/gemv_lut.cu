@@ -495,6 +495,38 @@ __global__ void __launch_bounds__(256) gemv_combine_kernel(const float* __restri
   if (threadIdx.x == 0) MBOK_COMBINE_STAMP(stamp_slot, 2);
 }
 
+// h[r] = silu(sum of the gate matrix's partials of row r) * (the up matrix's):
+// the gated feed-forward block's combine (each matrix's partials [nslab][mpad],
+// added in slab order as above).  The two matrices' loads of a round are all
+// issued before any is added; eight slabs a round keep the register count at
+// which a CTA of this grid fits beside the next layer's main CTA.
+template <bool HBF16>
+__global__ void __launch_bounds__(256) gemv_combine_gated_kernel(const float* __restrict__ pgate,
+                                                                 const float* __restrict__ pup, void* h, int M,
+                                                                 int mpad, int nslab) {
+  allow_dependents();
+  grid_dependency_wait();
+  const int r = blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= M) return;
+  float g = 0.f, u = 0.f;
+  for (int t0 = 0; t0 < nslab; t0 += 8) {
+    float a[8], b[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const size_t i = size_t(t0 + t) * mpad + r;
+      a[t] = t0 + t < nslab ? __ldcg(pgate + i) : 0.f;
+      b[t] = t0 + t < nslab ? __ldcg(pup + i) : 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (t0 + t < nslab) {
+        g += a[t];
+        u += b[t];
+      }
+  }
+  store_act(h, HBF16, size_t(r), gated(g, u));
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -637,40 +669,44 @@ size_t gemv_multi_workspace_bytes(int nseg, const int* K, const int* M, int N) {
   return total;
 }
 
-// y[0 .. sum M) = the matrices' outputs one after another, for one vector.
-// The row ranges per slab (cps) are shared out over the matrices by their
-// packed bytes (M_s * K_s), so one launch fills the SMs about as a single
-// matrix of the summed size would.
-cudaError_t launch_gemv_lut_multi(int nseg, const uint8_t* const* packed, const uint16_t* const* alpha, const int* K,
-                                  const int* M, int N, const void* x, bool x_f32, float* y, void* workspace,
-                                  cudaStream_t stream, bool weights_static) {
-  if (nseg < 1 || nseg > kMaxSegments) return cudaErrorInvalidValue;
+// Partial sums of the gated form: both matrices' regions, also with one slab
+// (the projections meet only in the combine).
+size_t gemv_gated_workspace_bytes(const Shape& s) {
+  const size_t nslab = size_t((s.N + kSlabCols - 1) / kSlabCols);
+  return 2 * nslab * size_t(s.O) * kOctet * sizeof(float);
+}
+
+// The main launch for several matrices sharing x, one vector: matrix i writes
+// its partial sums to partial[i] ([nslab][O_i * 8]) or, with one slab, its
+// outputs to y[i].  The row ranges per slab (cps) are shared out over the
+// matrices by their packed bytes (M_i * K_i), so one launch fills the SMs
+// about as a single matrix of the summed size would.
+static cudaError_t launch_multi_main(int nseg, const uint8_t* const* packed, const uint16_t* const* alpha,
+                                     const Shape* shapes, const void* x, bool x_f32, float* const* y,
+                                     float* const* partial, cudaStream_t stream, bool weights_static) {
   const int sm = device_sm_count();
-  const int nslab = (N + kSlabCols - 1) / kSlabCols;
+  const int nslab = (shapes[0].N + kSlabCols - 1) / kSlabCols;
   double wsum = 0.0;
-  for (int i = 0; i < nseg; ++i) wsum += double(M[i]) * K[i];
+  for (int i = 0; i < nseg; ++i) wsum += double(shapes[i].M) * shapes[i].K;
   const int budget = sm / nslab > nseg ? sm / nslab : nseg;   // row ranges per slab, all matrices together
   GemvMultiParams mp;
-  CombineMultiParams cm;
-  mp.nseg = cm.nseg = nseg;
-  cm.nvs = nslab;
-  int cta = 0, row = 0, max_k = 1;
-  size_t poff = 0;
+  mp.nseg = nseg;
+  int cta = 0, max_k = 1;
   size_t launch_bytes = 0;
-  for (int i = 0; i < nseg; ++i) launch_bytes += size_t(make_shape(K[i], M[i], N).O) * kOctet * K[i] * (N / 8);
+  for (int i = 0; i < nseg; ++i) launch_bytes += size_t(shapes[i].O) * kOctet * shapes[i].K * (shapes[i].N / 8);
   const bool early = stage_early(weights_static, launch_bytes);
   for (int i = 0; i < nseg; ++i) {
-    const Shape s = make_shape(K[i], M[i], N);
+    const Shape& s = shapes[i];
     GemvParams& p = mp.seg[i];
     p.packed = packed[i];
     p.alpha = alpha[i];
     p.s_in = nullptr;
     p.s_out = nullptr;
     p.x = x;
-    p.y = y + row;
+    p.y = y[i];
     p.s = s;
     p.nslab = nslab;
-    int cps = int(double(budget) * double(M[i]) * K[i] / wsum);
+    int cps = int(double(budget) * double(s.M) * s.K / wsum);
     if (cps < 1) cps = 1;
     if (cps > s.O) cps = s.O;
     p.cps = cps;
@@ -679,18 +715,12 @@ cudaError_t launch_gemv_lut_multi(int nseg, const uint8_t* const* packed, const 
     p.stamp_slot = 0;
     p.prefetch_octets = prefetch_depth(launch_bytes);
     p.sv_scales_staged = 0;
-    p.partial = nslab > 1 ? static_cast<float*>(workspace) + poff : nullptr;
+    p.partial = partial[i];
     mp.cta0[i] = cta;
-    cm.partial[i] = p.partial;
-    cm.row0[i] = row;
-    cm.mpad[i] = s.O * kOctet;
     cta += nslab * cps;
-    row += M[i];
-    if (nslab > 1) poff += size_t(nslab) * s.O * kOctet;
-    if (K[i] > max_k) max_k = K[i];
+    if (s.K > max_k) max_k = s.K;
   }
   mp.cta0[nseg] = cta;
-  cm.row0[nseg] = row;
 
   auto fn = x_f32 ? gemv_lut8_multi_kernel<true> : gemv_lut8_multi_kernel<false>;
   static PerDeviceOnce attr_once[2];   // per variant; the attributes are per device context
@@ -711,18 +741,76 @@ cudaError_t launch_gemv_lut_multi(int nseg, const uint8_t* const* packed, const 
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, fn, mp);
+  return cudaLaunchKernelEx(&cfg, fn, mp);
+}
+
+// A combine launch of one thread per row (dependent launch, 256 threads).
+template <class... Params, class... Args>
+static cudaError_t launch_combine(void (*fn)(Params...), int rows, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((rows + 255) / 256);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// y[0 .. sum M) = the matrices' outputs one after another, for one vector.
+cudaError_t launch_gemv_lut_multi(int nseg, const uint8_t* const* packed, const uint16_t* const* alpha, const int* K,
+                                  const int* M, int N, const void* x, bool x_f32, float* y, void* workspace,
+                                  cudaStream_t stream, bool weights_static) {
+  if (nseg < 1 || nseg > kMaxSegments) return cudaErrorInvalidValue;
+  const int nslab = (N + kSlabCols - 1) / kSlabCols;
+  Shape shapes[kMaxSegments];
+  float* ys[kMaxSegments];
+  float* partial[kMaxSegments];
+  CombineMultiParams cm;
+  cm.nseg = nseg;
+  cm.nvs = nslab;
+  int row = 0;
+  size_t poff = 0;
+  for (int i = 0; i < nseg; ++i) {
+    shapes[i] = make_shape(K[i], M[i], N);
+    ys[i] = y + row;
+    partial[i] = nslab > 1 ? static_cast<float*>(workspace) + poff : nullptr;
+    cm.partial[i] = partial[i];
+    cm.row0[i] = row;
+    cm.mpad[i] = shapes[i].O * kOctet;
+    row += M[i];
+    if (nslab > 1) poff += size_t(nslab) * shapes[i].O * kOctet;
+  }
+  cm.row0[nseg] = row;
+  cudaError_t e = launch_multi_main(nseg, packed, alpha, shapes, x, x_f32, ys, partial, stream, weights_static);
   if (e != cudaSuccess) return e;
   if (nslab > 1) {
-    cudaLaunchConfig_t c2 = {};
-    c2.gridDim = dim3((row + 255) / 256);
-    c2.blockDim = dim3(256);
-    c2.stream = stream;
-    c2.attrs = attr;
-    c2.numAttrs = 1;
-    e = cudaLaunchKernelEx(&c2, gemv_combine_multi_kernel, cm, y);
+    e = launch_combine(gemv_combine_multi_kernel, row, stream, cm, y);
     if (e != cudaSuccess) return e;
   }
+  return cudaGetLastError();
+}
+
+// h = silu(W_gate x) * (W_up x) for one vector; workspace as sized by
+// gemv_gated_workspace_bytes.  With one slab the main launch's outputs (not
+// partials) go to the workspace, which the combine reads the same way.
+cudaError_t launch_gemv_lut_gated(const uint8_t* packed_gate, const uint16_t* alpha_gate, const Shape& gate,
+                                  const uint8_t* packed_up, const uint16_t* alpha_up, const Shape& up, const void* x,
+                                  bool x_f32, void* h, bool h_bf16, void* workspace, cudaStream_t stream,
+                                  bool weights_static) {
+  const int nslab = (gate.N + kSlabCols - 1) / kSlabCols;
+  const int mpad = gate.O * kOctet;
+  const uint8_t* packed[2] = {packed_gate, packed_up};
+  const uint16_t* alpha[2] = {alpha_gate, alpha_up};
+  const Shape shapes[2] = {gate, up};
+  float* part[2] = {static_cast<float*>(workspace), static_cast<float*>(workspace) + size_t(nslab) * mpad};
+  cudaError_t e = launch_multi_main(2, packed, alpha, shapes, x, x_f32, part, part, stream, weights_static);
+  if (e != cudaSuccess) return e;
+  e = launch_combine(h_bf16 ? gemv_combine_gated_kernel<true> : gemv_combine_gated_kernel<false>, gate.M, stream,
+                     static_cast<const float*>(part[0]), static_cast<const float*>(part[1]), h, gate.M, mpad, nslab);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 

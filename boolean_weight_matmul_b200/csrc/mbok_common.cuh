@@ -56,6 +56,16 @@ __device__ __forceinline__ float2 half2_bits_to_float2(uint32_t h2) {
   return __half22float2(h);
 }
 
+// silu(g) * u in fp32: g / (1 + exp(-g)) * u.  exp(-g) overflows to infinity
+// for g below about -88, where the quotient is the 0 that silu tends to.
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + expf(-g)) * u; }
+
+// v as element i of an activation array, fp32 or rounded once to bf16.
+__device__ __forceinline__ void store_act(void* out, bool bf16, size_t i, float v) {
+  if (bf16) static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(out)[i] = v;
+}
+
 // The current device index, or -1 if the runtime cannot say.
 inline int current_device() {
   int dev = -1;

@@ -73,6 +73,9 @@ typedef enum { MBOK_F32 = 0, MBOK_BF16 = 1 } mbok_dtype;
 #define MBOK_GEMV_TENSOR 2
 #define MBOK_GEMV_LOOKUP_SLABS 3
 #define MBOK_GEMV_LOOKUP_ROWS 4
+/* Longest teacher list per token and largest vocabulary of mbok_distill_*. */
+#define MBOK_DISTILL_MAX_TOP 512
+#define MBOK_DISTILL_MAX_VOCAB (1 << 21)
 /* Size of the scratch array built into the library for mbok_gemv_noalloc. */
 #define MBOK_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -265,6 +268,79 @@ size_t mbok_gemv_multi_workspace_bytes(int nseg, const int* K, const int* M, int
 int mbok_gemv_multi(int nseg, const uint32_t* const* packed, const uint16_t* const* alpha, const int* K,
                     const int* M, int N, int group, const void* x, int x_dtype, int batch, float* y,
                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace mbok_gemv_gated needs (same rules as
+ * mbok_gemv_workspace_bytes): both projections' partial sums for one vector,
+ * 0 for more.  0 on a bad argument. */
+size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int batch);
+
+/* The gated feed-forward block's first half for a decode step: two
+ * projections of x, one gating the other,
+ *     h[b][r] = silu(g) * u,   g = sum_j W_gate[r][j] x[b][j],
+ *     u = sum_j W_up[r][j] x[b][j],   silu(g) = g / (1 + exp(-g)),
+ * without storing g and u.  Each matrix has its own number of kernels; both
+ * have M rows.
+ *   h       : [batch][M], fp32 (h_dtype MBOK_F32) or bf16 (MBOK_BF16, each
+ *             value rounded once), aligned to its element, fully overwritten.
+ *   Other arguments as mbok_gemv (workspace sized by
+ *   mbok_gemv_gated_workspace_bytes; mbok_gemv_set_static_weights applies).
+ * One vector runs on the lookup kernel (one launch over both matrices and the
+ * small launch that adds the slabs' partials and gates), two to 16 on the
+ * tensor-core kernel (one launch per 16 bf16 or 5 fp32 vectors).
+ * g and u have the accuracy of mbok_gemv; deterministic. */
+int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
+                    const uint16_t* alpha_up, int K_up, int M, int N, int group, const void* x, int x_dtype, int batch,
+                    void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of the gate of mbok_gemm_gated: from dH = dL/dH and the two
+ * projections that call kept,
+ *     dgate = dH u s (1 + g (1 - s)),   dup = dH g s,   s = 1 / (1 + exp(-g)),
+ * and, with H given, H = g s u again (for the gradient of the projection
+ * that reads H, so that it need not be kept).
+ *   dH, gate, up    : bf16 [T][M].
+ *   dgate, dup, H   : out, bf16 [T][M], rounded once each; H may be NULL.  An
+ *                     output may be one of the inputs (the same address).
+ * All 16-byte aligned.  1 <= T <= 2^23, 1 <= M <= 2^22. */
+int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t* up, int T, int M, uint16_t* dgate,
+                        uint16_t* dup, uint16_t* H, void* stream);
+
+/* Distillation from a teacher's top logits: fine-tuning a converted model by
+ * a KL loss on the logits of its full-precision teacher (Italian technical
+ * summary 2C), of which only the `top` largest per token are stored.  Per
+ * token t, with temperature tau,
+ *     p   = softmax of teacher[t][i] / tau over the listed entries,
+ *     q   = softmax of logits[t][j] / tau over j < V,
+ *     lse[t]  = log sum_j exp(logits[t][j] / tau),
+ *     loss[t] = weight[t] sum_i p_i (log p_i - log q[index[t][i]]),
+ *     dlogits[t][j] = weight[t] / tau (q_j - sum of p_i with index[t][i] = j).
+ * An entry whose index lies outside [0, V) (say -1, padding a short list) or
+ * whose teacher logit is -infinity is not listed; an index given twice counts
+ * twice.  A token of weight 0, or with nothing listed, has loss 0, lse 0 and
+ * gradient 0 whatever its logits.  Logits of -infinity have probability 0; a
+ * row with no other, or with +infinity or NaN, gives NaN.
+ *   logits  : fp32 (dtype MBOK_F32) or bf16 (MBOK_BF16) [T][V], rows `ld`
+ *             elements apart (ld >= V), 16-byte aligned (the first row).
+ *   teacher : fp32 [T][top].   index: int32 [T][top].   1 <= top <= MBOK_DISTILL_MAX_TOP.
+ *   temperature : 2^-10 .. 2^10.
+ *   weight  : fp32 [T], or NULL for 1.
+ *   loss, lse : out, fp32 [T].
+ *   dlogits : out, as logits with rows ld_dlogits apart, or NULL for the loss
+ *             alone; may be `logits` itself (then with the same ld).
+ * With dlogits each logit is read once for rows of up to 262144 bf16 or
+ * 131072 fp32 values.  Sums are fp32 in a fixed order: deterministic.
+ * 1 <= T <= 2^23, 1 <= V <= MBOK_DISTILL_MAX_VOCAB. */
+int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
+                      const int32_t* index, int top, float temperature, const float* weight, float* loss, float* lse,
+                      void* dlogits, size_t ld_dlogits, void* stream);
+
+/* The gradient alone, from the lse that mbok_distill_loss returned for the
+ * same arguments and the gradient of the loss that followed:
+ *     dlogits[t][j] = grad[t] weight[t] / tau (q_j - sum of p_i with index[t][i] = j),
+ * q_j = exp(logits[t][j] / tau - lse[t]).  grad: fp32 [T], or NULL for 1.
+ * Other arguments as mbok_distill_loss. */
+int mbok_distill_backward(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
+                          const int32_t* index, int top, float temperature, const float* weight, const float* lse,
+                          const float* grad, void* dlogits, size_t ld_dlogits, void* stream);
 
 /* Kernel choice of mbok_gemv and mbok_gemv_noalloc for this process (all
  * devices, all later calls):

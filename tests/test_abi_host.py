@@ -229,3 +229,61 @@ def test_gemv_ex_argument_checks(L):
     assert L.mbok_gemv_ex(P, P, 3, 64, 512, 128, P, 1, 1, P, P, 1 << 20, -1, 1, None) == 1
     assert L.mbok_gemv_ex(P, P, 3, 64, 512, 128, P, 1, 1, P, P, 1 << 20, 1, 2, None) == 1
     assert L.mbok_gemv_ex(P, P, 3, 64, 500, 128, P, 1, 1, P, P, 1 << 20, 1, 1, None) == 2
+
+
+def test_gemv_gated_sizes_and_argument_errors(L):
+    O = lambda M: (M + 7) // 8
+    # both projections' partials [N/512 slabs][O * 8], with one slab too; none for more than one vector
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 1) == 2 * 8 * O(100) * 8 * 4
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 128, 1) == 2 * O(100) * 8 * 4
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 2) == 0
+    assert L.mbok_gemv_gated_workspace_bytes(0, 2, 100, 4096, 1) == 0
+    g = lambda **kw: L.mbok_gemv_gated(*[kw.get(k, v) for k, v in dict(
+        pg=FAKE, ag=FAKE, Kg=3, pu=FAKE, au=FAKE, Ku=2, M=64, N=1024, group=128, x=FAKE, dt=1, batch=1, h=FAKE, hd=1,
+        ws=FAKE, wsb=1 << 20, stream=None).items()])
+    assert g(Kg=0) == 1 and g(Ku=5) == 1 and g(M=0) == 2 and g(N=100) == 2 and g(group=64) == 4
+    for name in ("pg", "ag", "pu", "au", "x", "h"):
+        assert g(**{name: None}) == 1
+    for name in ("pg", "ag", "pu", "au", "x"):
+        assert g(**{name: FAKE + 8}) == 3
+    assert g(h=FAKE_ODD) == 3 and g(h=FAKE + 2, hd=0) == 3
+    assert g(dt=7) == 1 and g(hd=2) == 1 and g(batch=0) == 1 and g(batch=17) == 1
+    assert g(ws=None) == 6 and g(wsb=16) == 6 and g(ws=FAKE + 4) == 6
+
+
+def test_gated_backward_argument_errors(L):
+    g = lambda **kw: L.mbok_gated_backward(*[kw.get(k, v) for k, v in dict(
+        dH=FAKE, gate=FAKE, up=FAKE, T=4, M=64, dg=FAKE, du=FAKE, H=None, stream=None).items()])
+    assert g(T=0) == 2 and g(M=0) == 2 and g(T=1 << 24) == 2 and g(M=1 << 23) == 2 and g(T=1 << 23, M=1 << 22) == 2
+    for name in ("dH", "gate", "up", "dg", "du"):
+        assert g(**{name: None}) == 1 and g(**{name: FAKE + 2}) == 3
+    assert g(H=FAKE + 8) == 3
+
+
+def test_distill_argument_errors(L):
+    base = dict(z=FAKE, dt=0, T=4, V=100, ld=100, teacher=FAKE, index=FAKE, top=8, tau=1.0, weight=FAKE, loss=FAKE,
+                lse=FAKE, dz=FAKE, ldz=100, stream=None)
+    g = lambda **kw: L.mbok_distill_loss(*[kw.get(k, v) for k, v in base.items()])
+    back = dict(z=FAKE, dt=0, T=4, V=100, ld=100, teacher=FAKE, index=FAKE, top=8, tau=1.0, weight=None, lse=FAKE,
+                grad=None, dz=FAKE + 4096, ldz=100, stream=None)
+    b = lambda **kw: L.mbok_distill_backward(*[kw.get(k, v) for k, v in back.items()])
+    for f in (g, b):
+        assert f(dt=2) == 1 and f(T=0) == 2 and f(V=0) == 2 and f(V=(1 << 21) + 1, ld=1 << 22) == 2 and f(ld=99) == 2
+        assert f(top=0) == 1 and f(top=513) == 1
+        assert f(tau=0.0) == 1 and f(tau=-1.0) == 1 and f(tau=float("nan")) == 1 and f(tau=float("inf")) == 1
+        for name in ("z", "teacher", "index", "lse"):
+            assert f(**{name: None}) == 1
+        assert f(z=FAKE + 8) == 3 and f(teacher=FAKE_ODD) == 3 and f(index=FAKE + 2) == 3 and f(dz=FAKE + 8) == 3
+        assert f(ldz=99) == 2
+        assert f(dz=FAKE, ld=104, ldz=100) == 2      # in place with another row distance
+    assert g(loss=None) == 1 and b(dz=None) == 1 and b(grad=FAKE_ODD) == 3 and g(weight=FAKE_ODD) == 3
+
+
+def test_finetune_binding_refuses_cpu_tensors(L):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    t = torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mb.gated_backward(t, t, t, 1, 64, t, t)
+    with pytest.raises(ValueError):
+        mb.distill_loss(t, mb.BF16, 1, 64, 64, t, t, 1, 1.0, None, t, t)

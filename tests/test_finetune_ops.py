@@ -1,0 +1,390 @@
+"""Gated feed-forward and fine-tuning calls on the GPU against an fp64 oracle
+(oracle/finetune_oracle.py), at the sizes and masks where they can go wrong.
+
+Tolerances, derived before the first run:
+ * a sum of n fp32 terms taken in any order is off by at most n 2^-24 times the
+   sum of their absolute values (GAMMA below);
+ * an output rounded once to type t adds half a step, finfo(t).eps / 2 of its
+   value (HALF below);
+ * what else a formula adds is said where its tolerance is formed."""
+import numpy as np
+import pytest
+
+from boolean_weight_matmul_b200 import workloads as wl
+from oracle import finetune_oracle as F
+from oracle import mbok_oracle as O
+from helpers import alpha_blocked_gpu, ensure_built, guarded, packed_from_signs_gpu, to_dev, x_dev
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+def gamma(n):
+    return n * 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    ensure_built()
+
+
+def _dt(name):
+    import torch
+    return torch.float32 if name == "f32" else torch.bfloat16
+
+
+def _code(name):
+    import boolean_weight_matmul_b200 as mb
+    return mb.F32 if name == "f32" else mb.BF16
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _assert_within(got, want, tol, what=""):
+    got, want = np.asarray(got, dtype=np.float64), np.asarray(want)
+    ok = np.abs(got - want) <= tol
+    if not ok.all():
+        bad = tuple(np.argwhere(~ok)[0])
+        raise AssertionError(f"{what}: {int((~ok).sum())} of {ok.size} out of tolerance, e.g. {bad} got {got[bad]} "
+                             f"want {want[bad]} tolerance {np.broadcast_to(tol, got.shape)[bad]}")
+
+
+class Layer:
+    """One matrix: host signs and scales, and their device forms."""
+
+    def __init__(self, K, M, N, seed, pad_nan=False):
+        import torch
+        self.K, self.M, self.N = K, M, N
+        signs = wl.random_signs(K, M, N, seed)
+        self.alpha = wl.alpha_decaying(K, M, N, seed + 1)
+        self.words = O.pack_signs(signs)
+        self.packed = packed_from_signs_gpu(signs)
+        self.blocked = alpha_blocked_gpu(self.alpha, K, M, N)
+        if pad_nan and M % 8:
+            # the rows that pad the last octet hold anything: every reader ignores them
+            self.blocked.view(-1, N // 128, K, 8)[-1, :, :, M % 8:] = float("nan")
+            torch.cuda.synchronize()
+
+    def host(self):
+        return self.words, self.alpha, self.K, self.M
+
+
+# ---- gated decode ------------------------------------------------------------
+
+def _x(batch, N, seed, dtype):
+    x = wl.x_normal(batch, N, seed, dtype)
+    return x, (x.astype(np.float64) if dtype == "f32" else wl.bf16_bits_to_f32(x).astype(np.float64))
+
+
+def _gated_tol(g, Eg, u, Eu, n, h, out):
+    # g and u are sums of n terms; |silu'| < 1.1; expf, the division and the
+    # product add at most 2^-20 of the value, expf's argument |g| 2^-24 more
+    e = 1.1 * np.abs(u) * gamma(n) * Eg + np.abs(F.silu(g)) * gamma(n) * Eu
+    return e * 1.01 + np.abs(h) * (2.0 ** -20 + np.abs(g) * 2.0 ** -23 + HALF[out]) + 1e-30
+
+
+def _gemv_gated(gate, up, xd, x_dtype, batch, out):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    h = guarded((batch, gate.M), _dt(out))
+    ws = mb.empty_gated_workspace(gate.K, up.K, gate.M, gate.N, batch)
+    ws.fill_(0xFF)   # NaN: nothing may be read before it is written
+    mb.gemv_gated(gate.packed, gate.blocked, gate.K, up.packed, up.blocked, up.K, gate.M, gate.N, 128, xd,
+                  _code(x_dtype), batch, h, _code(out), ws)
+    torch.cuda.synchronize()
+    assert mb.read_device_errors() == 0
+    return h
+
+
+@pytest.mark.parametrize("kg,ku", [(1, 1), (3, 3), (4, 1), (2, 4)])
+@pytest.mark.parametrize("M,N", [(1, 128), (7, 512), (13, 640), (129, 1024), (200, 4224)])
+@pytest.mark.parametrize("batch", [1, 2, 5, 16])
+def test_gemv_gated(kg, ku, M, N, batch):
+    gate, up = Layer(kg, M, N, 9000 + kg + M, pad_nan=True), Layer(ku, M, N, 9100 + ku + N, pad_nan=True)
+    for x_dtype, out in (("bf16", "bf16"), ("f32", "f32")):
+        x, x64 = _x(batch, N, 77 + batch, x_dtype)
+        h = _gemv_gated(gate, up, x_dev(x, x_dtype), x_dtype, batch, out)
+        g, Eg = F.project(gate.words, gate.alpha, kg, M, N, x64)
+        u, Eu = F.project(up.words, up.alpha, ku, M, N, x64)
+        want = F.silu(g) * u
+        _assert_within(_f64(h), want, _gated_tol(g, Eg, u, Eu, N * max(kg, ku), want, out), f"{x_dtype} -> {out}")
+
+
+def test_gemv_gated_mixed_types_and_alignment():
+    # fp32 in, bf16 out and the other way round; an output at an odd element
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    K, M, N, batch = 3, 77, 1152, 3
+    gate, up = Layer(K, M, N, 1), Layer(K, M, N, 2)
+    for x_dtype, out in (("f32", "bf16"), ("bf16", "f32")):
+        x, x64 = _x(batch, N, 3, x_dtype)
+        g, Eg = F.project(gate.words, gate.alpha, K, M, N, x64)
+        u, Eu = F.project(up.words, up.alpha, K, M, N, x64)
+        want = F.silu(g) * u
+        buf = guarded((batch * M + 1,), _dt(out))
+        first = buf[:1].clone()
+        h = buf[1:].view(batch, M)
+        mb.gemv_gated(gate.packed, gate.blocked, K, up.packed, up.blocked, K, M, N, 128, x_dev(x, x_dtype),
+                      _code(x_dtype), batch, h, _code(out), None)
+        torch.cuda.synchronize()
+        _assert_within(_f64(h), want, _gated_tol(g, Eg, u, Eu, N * K, want, out))
+        assert torch.equal(first.view(torch.uint8), buf[:1].view(torch.uint8))
+
+
+def test_gemv_gated_extremes():
+    # a gate far below zero closes (0), far above passes u; a NaN reaches only its vector
+    import torch
+    K, M, N, batch = 1, 16, 256, 2
+    gate, up = Layer(K, M, N, 11), Layer(K, M, N, 12)
+    x, _ = _x(batch, N, 13, "f32")
+    x *= 1e4
+    x[1, 5] = np.nan
+    for rows in (1, 2):
+        h = _gemv_gated(gate, up, to_dev(x[:rows]), "f32", rows, "f32")
+        g, _ = F.project(gate.words, gate.alpha, K, M, N, x[:1].astype(np.float64))
+        u, _ = F.project(up.words, up.alpha, K, M, N, x[:1].astype(np.float64))
+        got = _f64(h)[0]
+        assert np.isfinite(got).all()
+        closed = g[0] < -200
+        assert closed.any() and (got[closed] == 0).all()
+        opened = g[0] > 200
+        assert opened.any()
+        _assert_within(got[opened], (g * u)[0][opened], np.abs(g * u)[0][opened] * 1e-3)
+        if rows == 2:
+            assert torch.isnan(h[1]).all()
+
+
+def test_gemv_gated_deterministic_and_graph():
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    gate, up = Layer(3, 520, 2048, 21), Layer(2, 520, 2048, 22)
+    for batch in (1, 7):
+        x, _ = _x(batch, 2048, 23, "bf16")
+        xd = x_dev(x, "bf16")
+        first = _gemv_gated(gate, up, xd, "bf16", batch, "bf16").clone()
+        h = torch.zeros(batch, 520, dtype=torch.bfloat16, device="cuda")
+        ws = mb.empty_gated_workspace(3, 2, 520, 2048, batch)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mb.gemv_gated(gate.packed, gate.blocked, 3, up.packed, up.blocked, 2, 520, 2048, 128, xd, mb.BF16, batch, h,
+                          mb.BF16, ws)
+        for _ in range(3):
+            h.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(h, first)
+
+
+# ---- the gate's gradient -------------------------------------------------------
+
+@pytest.mark.parametrize("T,M", [(1, 1), (1, 7), (3, 5), (33, 1001), (64, 4096)])
+@pytest.mark.parametrize("remake", [False, True])
+def test_gated_backward(T, M, remake):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    rng = np.random.default_rng(T * M)
+    host = [rng.standard_normal((T, M)) * s for s in (0.3, 4.0, 2.0)]
+    host[1].flat[0] = -100.0
+    host[1].flat[-1] = 90.0
+    dev = [torch.from_numpy(a).to(torch.bfloat16).cuda() for a in host]
+    dh, g, u = (_f64(t) for t in dev)
+    out = [guarded((T, M), torch.bfloat16) for _ in range(3)]
+    mb.gated_backward(*dev, T, M, out[0], out[1], out[2] if remake else None)
+    torch.cuda.synchronize()
+    dg, du, h, E = F.gated_grad(dh, g, u)
+    # the exponential and the reciprocal: a few fp32 steps and |g| 2^-23 of each term
+    rel = 2.0 ** -20 + np.abs(g) * 2.0 ** -22
+    tiny = 1e-36   # a sigmoid below 2^-126 may come out as 0
+    _assert_within(_f64(out[0]), dg, E * rel + np.abs(dg) * HALF["bf16"] + tiny, "dgate")
+    _assert_within(_f64(out[1]), du, np.abs(du) * (rel + HALF["bf16"]) + tiny, "dup")
+    if remake:
+        _assert_within(_f64(out[2]), h, np.abs(h) * (rel + HALF["bf16"]) + tiny, "h")
+
+
+def test_gated_backward_in_place_and_differences():
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    rng = np.random.default_rng(5)
+    T, M = 9, 123
+    dh, g, u = (torch.from_numpy(rng.standard_normal((T, M))).to(torch.bfloat16).cuda() for _ in range(3))
+    a, b, c = (torch.empty_like(g) for _ in range(3))
+    mb.gated_backward(dh, g, u, T, M, a, b, c)
+    x, y, z = dh.clone(), g.clone(), u.clone()
+    mb.gated_backward(x, y, z, T, M, y, z, x)
+    torch.cuda.synchronize()
+    assert torch.equal(a, y) and torch.equal(b, z) and torch.equal(c, x)
+    # against central differences of the formula
+    G, U, D = _f64(g), _f64(u), _f64(dh)
+    eps = 1e-5
+    dg = D * (F.silu(G + eps) - F.silu(G - eps)) * U / (2 * eps)
+    _assert_within(_f64(a), dg, np.abs(dg) * (HALF["bf16"] + 1e-4) + 1e-6)
+
+
+# ---- distillation --------------------------------------------------------------
+
+def _distill_case(T, V, top, seed, dtype, masked=True, ld=None):
+    import torch
+    rng = np.random.default_rng(seed)
+    ld = V if ld is None else ld
+    z = torch.from_numpy(rng.standard_normal((T, ld)) * 3).to(_dt(dtype))
+    teacher = (rng.standard_normal((T, top)) * 2 + 4).astype(np.float32)
+    index = np.stack([rng.permutation(V)[:top] if top <= V else rng.integers(0, V, top) for _ in range(T)]).astype(np.int32)
+    weight = rng.uniform(0.5, 1.5, T).astype(np.float32)
+    grad = rng.uniform(0.5, 1.5, T).astype(np.float32)
+    if masked and T > 3:
+        weight[1] = 0.0
+        index[2] = -1
+        index[3, top // 2:] = V + 5
+        teacher[0, 0] = -np.inf
+    return z, teacher, index, weight, grad
+
+
+def _check_distill(z, teacher, index, weight, grad, tau, V, dtype, got_loss, got_lse, got_dz):
+    z64 = z[:, :V].double().numpy()
+    loss, lse, dz, q, p = F.distill(z64, teacher.astype(np.float64), index, tau, weight.astype(np.float64),
+                                    grad.astype(np.float64))
+    live = lse != 0
+    y = np.where(np.isfinite(z64), z64, 0) / tau
+    span = (np.abs(y).max(1) + np.abs(lse) + np.abs(teacher[np.isfinite(teacher)]).max() / tau + 8)
+    # every exponent and logarithm is off by a few fp32 steps of its size: 2^-22 of the row's span
+    _assert_within(got_lse, lse, np.where(live, span * 2.0 ** -22, 0), "lse")
+    _assert_within(got_loss, loss, np.where(live, np.abs(weight) * span * 2.0 ** -21, 0), "loss")
+    scale = np.abs(grad * weight / tau)[:, None]
+    tol = scale * (q + p) * (span * 2.0 ** -21)[:, None] + np.abs(dz) * HALF[dtype] + 1e-38
+    _assert_within(got_dz, dz, np.where(live[:, None], tol, 0), "dz")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,top,tau", [(1, 1, 1, 1.0), (5, 7, 3, 2.0), (9, 1000, 16, 1.0), (4, 32001, 64, 2.0),
+                                         (6, 4099, 512, 3.5), (2, 128000, 20, 1.0), (5, 40, 64, 0.5)])
+def test_distill(dtype, T, V, top, tau):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    z, teacher, index, weight, grad = _distill_case(T, V, top, T + V + top, dtype)
+    zd = z.cuda()
+    td, xd, wd, gd = to_dev(teacher), to_dev(index), to_dev(weight), to_dev(grad)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    dz = guarded((T, V), _dt(dtype))
+    mb.distill_loss(zd, _code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse, dz, V)
+    torch.cuda.synchronize()
+    ones = np.ones_like(grad)
+    _check_distill(z, teacher, index, weight, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(dz))
+    # the loss alone, then the gradient from its lse
+    loss2, lse2, dz2 = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), _dt(dtype))
+    mb.distill_loss(zd, _code(dtype), T, V, V, td, xd, top, tau, wd, loss2, lse2)
+    mb.distill_backward(zd, _code(dtype), T, V, V, td, xd, top, tau, wd, lse2, gd, dz2, V)
+    torch.cuda.synchronize()
+    _check_distill(z, teacher, index, weight, grad, tau, V, dtype, _f64(loss2), _f64(lse2), _f64(dz2))
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_strides_and_in_place(dtype):
+    # rows that start anywhere in a 16-byte line, gradient rows with another
+    # offset, what lies between the rows left as it was, and the gradient in place
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top, tau = 7, 2053, 9, 2.0
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 3, dtype, ld=V + 4)
+    td, xd, wd = to_dev(teacher), to_dev(index), to_dev(weight)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    ones = np.ones_like(grad)
+    for ld_dz in (V, V + 3, V + 4):
+        buf = torch.full((T, ld_dz), 7.0, dtype=_dt(dtype), device="cuda")
+        mb.distill_loss(z.cuda(), _code(dtype), T, V, V + 4, td, xd, top, tau, wd, loss, lse, buf, ld_dz)
+        torch.cuda.synchronize()
+        _check_distill(z, teacher, index, weight, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(buf[:, :V]))
+        assert (buf[:, V:] == 7.0).all()
+    zd = z.cuda()
+    mb.distill_loss(zd, _code(dtype), T, V, V + 4, td, xd, top, tau, wd, loss, lse, zd, V + 4)
+    torch.cuda.synchronize()
+    assert torch.equal(zd[:, :V], buf[:, :V]) and torch.equal(zd[:, V:].cpu(), z[:, V:])
+    zd = z.cuda()
+    mb.distill_backward(zd, _code(dtype), T, V, V + 4, td, xd, top, tau, wd, lse, None, zd, V + 4)
+    torch.cuda.synchronize()
+    _check_distill(z, teacher, index, weight, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(zd[:, :V]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_same_index_twice_and_masked_logits(dtype):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top, tau = 4, 600, 12, 1.0
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 4, dtype, masked=False)
+    index[:, 5] = index[:, 2]
+    index[:, 7] = index[:, 2]
+    free = np.setdiff1d(np.arange(V), index.ravel())
+    z[0, free] = float("-inf")                       # masked by -infinity
+    z[1, free] = torch.finfo(z.dtype).min            # masked by the lowest value
+    z[2, free[:300]] = float("-inf")
+    td, xd = to_dev(teacher), to_dev(index)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    ones = np.ones(T, dtype=np.float32)
+    dz = guarded((T, V), _dt(dtype))
+    mb.distill_loss(z.cuda(), _code(dtype), T, V, V, td, xd, top, tau, None, loss, lse, dz, V)
+    torch.cuda.synchronize()
+    clean = z.clone()
+    clean[1, free] = float("-inf")
+    _check_distill(clean, teacher, index, ones, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(dz))
+    mb.distill_backward(z.cuda(), _code(dtype), T, V, V, td, xd, top, tau, None, lse, None, dz, V)
+    torch.cuda.synchronize()
+    _check_distill(clean, teacher, index, ones, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(dz))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_wide_rows(dtype):
+    # wider than a cluster's registers: the loss in several passes, the gradient from memory
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top, tau = 2, 300001, 5, 1.0
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 6, dtype, masked=False)
+    loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), _dt(dtype))
+    mb.distill_loss(z.cuda(), _code(dtype), T, V, V, to_dev(teacher), to_dev(index), top, tau, to_dev(weight), loss,
+                    lse, dz, V)
+    torch.cuda.synchronize()
+    _check_distill(z, teacher, index, weight, np.ones_like(grad), tau, V, dtype, _f64(loss), _f64(lse), _f64(dz))
+
+
+def test_distill_rows_without_use():
+    # no weight or nothing listed: zeros, whatever the logits hold; NaN logits elsewhere stay in their row
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top = 5, 333, 4
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 8, "f32", masked=False)
+    z[0, 3] = float("nan")
+    z[1, :] = float("nan")
+    z[2, :] = float("-inf")
+    weight[0] = 0.0
+    index[1] = -1
+    loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), torch.float32)
+    mb.distill_loss(z.cuda(), mb.F32, T, V, V, to_dev(teacher), to_dev(index), top, 1.0, to_dev(weight), loss, lse, dz, V)
+    torch.cuda.synchronize()
+    for t in (0, 1):
+        assert loss[t] == 0 and lse[t] == 0 and (dz[t] == 0).all()
+    assert torch.isnan(loss[2]) and torch.isnan(dz[2]).all()
+    assert torch.isfinite(dz[3:]).all() and torch.isfinite(loss[3:]).all()
+
+
+def test_distill_gradient_against_differences():
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top, tau = 2, 50, 6, 2.0
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 12, "f32", masked=False)
+    loss, lse, dz = (torch.empty(s, device="cuda") for s in ((T,), (T,), (T, V)))
+    mb.distill_loss(z.cuda(), mb.F32, T, V, V, to_dev(teacher), to_dev(index), top, tau, to_dev(weight), loss, lse, dz, V)
+    torch.cuda.synchronize()
+    z64, eps = z.double().numpy(), 1e-5
+    one = np.ones(T)
+    for j in range(V):
+        hi, lo = z64.copy(), z64.copy()
+        hi[:, j] += eps
+        lo[:, j] -= eps
+        args = (teacher.astype(np.float64), index, tau, weight.astype(np.float64), one)
+        d = (F.distill(hi, *args)[0] - F.distill(lo, *args)[0]) / (2 * eps)
+        _assert_within(_f64(dz[:, j]), d, 1e-6)
