@@ -77,6 +77,10 @@ def lib() -> ctypes.CDLL:
             "mbok_gemv_multi_workspace_bytes": ([i, vp, vp, i], sz),
             "mbok_gemv_gated_workspace_bytes": ([i, i, i, i, i], sz),
             "mbok_gemv_gated": ([vp, vp, i, vp, vp, i, i, i, i, vp, i, i, vp, i, vp, sz, vp], i),
+            "mbok_gemm_gated_workspace_bytes": ([i, i, i], sz),
+            "mbok_gemm_gated": ([vp, vp, i, vp, vp, i, i, i, i, vp, i, vp, vp, vp, vp, sz, vp], i),
+            "mbok_gemm_backward_workspace_bytes": ([i, vp, vp, i, i], sz),
+            "mbok_gemm_backward": ([i, vp, vp, vp, vp, i, i, vp, i, vp, vp, vp, vp, sz, vp], i),
             "mbok_gated_backward": ([vp, vp, vp, i, i, vp, vp, vp, vp], i),
             "mbok_distill_loss": ([vp, i, i, i, sz, vp, vp, i, f, vp, vp, vp, vp, sz, vp], i),
             "mbok_distill_backward": ([vp, i, i, i, sz, vp, vp, i, f, vp, vp, vp, vp, sz, vp], i),
@@ -292,6 +296,53 @@ def gemv_gated(packed_gate, alpha_gate, K_gate, packed_up, alpha_up, K_up, M, N,
     pg, ag, pu, au, px, ph, pws = _ptrs(packed_gate, alpha_gate, packed_up, alpha_up, x, h, workspace)
     _check(lib().mbok_gemv_gated(pg, ag, K_gate, pu, au, K_up, M, N, group, px, x_dtype, batch, ph, h_dtype, pws,
                                  _ws_bytes(workspace), _stream(stream)), "mbok_gemv_gated")
+
+
+def gemm_gated_workspace_bytes(M: int, N: int, T: int) -> int:
+    return int(lib().mbok_gemm_gated_workspace_bytes(M, N, T))
+
+
+def empty_gemm_gated_workspace(M: int, N: int, T: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(gemm_gated_workspace_bytes(M, N, T), 256), dtype=torch.uint8, device=device)
+
+
+def gemm_gated(packed_gate, alpha_gate, K_gate, packed_up, alpha_up, K_up, M, N, group, X, T, H, gate, up, workspace,
+               stream=None) -> None:
+    """H = silu(X W_gate^T) * (X W_up^T) for T tokens; gate and up, if given,
+    receive the two projections for gated_backward (see include/mbok.h)."""
+    pg, ag, pu, au, px, ph, qg, qu, pws = _ptrs(packed_gate, alpha_gate, packed_up, alpha_up, X, H, gate, up, workspace)
+    _check(lib().mbok_gemm_gated(pg, ag, K_gate, pu, au, K_up, M, N, group, px, T, ph, qg, qu, pws,
+                                 _ws_bytes(workspace), _stream(stream)), "mbok_gemm_gated")
+
+
+def gemm_backward_workspace_bytes(K_list, M_list, N: int, T: int) -> int:
+    ka, kp = _int_array(K_list)
+    ma, mp = _int_array(M_list)
+    return int(lib().mbok_gemm_backward_workspace_bytes(len(K_list), kp, mp, N, T))
+
+
+def empty_gemm_backward_workspace(K_list, M_list, N: int, T: int, device="cuda") -> torch.Tensor:
+    return torch.empty(max(gemm_backward_workspace_bytes(K_list, M_list, N, T), 256), dtype=torch.uint8, device=device)
+
+
+def gemm_backward(packed_list, alpha_list, K_list, M_list, N, group, X, T, dY_list, dX, dalpha_list, workspace,
+                  stream=None) -> None:
+    """Backward pass of layers that share X: dX (or None) and each matrix's
+    scale gradient (dalpha_list or an entry of it may be None; see
+    include/mbok.h)."""
+    n = len(packed_list)
+    if dalpha_list is None:
+        dalpha_list = [None] * n
+    if not (len(alpha_list) == len(K_list) == len(M_list) == len(dY_list) == len(dalpha_list) == n):
+        raise ValueError("gemm_backward: one packed, alpha, K, M, dY and dalpha per matrix")
+    ptrs = _ptrs(*packed_list, *alpha_list, *dY_list, *dalpha_list, X, dX, workspace)
+    arrays = [(ctypes.c_void_p * n)(*ptrs[i * n:(i + 1) * n]) for i in range(4)]
+    pp, pa, py, pd = (ctypes.cast(a, ctypes.c_void_p) for a in arrays)
+    px, pdx, pws = ptrs[4 * n:]
+    ka, kp = _int_array(K_list)
+    ma, mp = _int_array(M_list)
+    _check(lib().mbok_gemm_backward(n, pp, pa, kp, mp, N, group, px, T, py, pdx, pd, pws, _ws_bytes(workspace),
+                                    _stream(stream)), "mbok_gemm_backward")
 
 
 def gated_backward(dH, gate, up, T, M, dgate, dup, H=None, stream=None) -> None:

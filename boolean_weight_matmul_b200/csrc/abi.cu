@@ -42,6 +42,15 @@ cudaError_t launch_gemv_gated(const uint8_t*, const uint16_t*, const Shape&, con
 unsigned gemv_gated_error_flags();
 cudaError_t launch_gated_backward(const uint16_t*, const uint16_t*, const uint16_t*, size_t, uint16_t*, uint16_t*,
                                   uint16_t*, cudaStream_t);
+size_t gemm_gated_workspace_bytes(int, int);
+cudaError_t launch_gemm_gated(const uint8_t*, const uint16_t*, const Shape&, const uint8_t*, const uint16_t*,
+                              const Shape&, const uint16_t*, int, uint16_t*, uint16_t*, uint16_t*, void*,
+                              cudaStream_t);
+size_t gemm_backward_workspace_bytes(int, const Shape*, int);
+cudaError_t launch_gemm_backward(int, const uint8_t* const*, const uint16_t* const*, const Shape*, const uint16_t*,
+                                 int, const uint16_t* const*, uint16_t*, float* const*, void*, cudaStream_t);
+unsigned gemm_pair_error_flags();
+unsigned gemm_dalpha_error_flags();
 cudaError_t launch_distill_loss(const void*, bool, int, int, size_t, const float*, const int*, int, float,
                                 const float*, float*, float*, void*, size_t, cudaStream_t);
 cudaError_t launch_distill_backward(const void*, bool, int, int, size_t, const float*, const int*, int, float,
@@ -351,6 +360,71 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
   return from_cuda(launch_gated_backward(dH, gate, up, n, dgate, dup, H, as_stream(stream)));
 }
 
+size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T) {
+  if (check_shape(1, M, N) != MBOK_OK || T < 1 || T > kMaxTokens) return 0;
+  return gemm_gated_workspace_bytes(N, T);
+}
+
+int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
+                    const uint16_t* alpha_up, int K_up, int M, int N, int group, const uint16_t* X, int T, uint16_t* H,
+                    uint16_t* gate, uint16_t* up, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_shape(K_gate, M, N);
+  if (st == MBOK_OK) st = check_shape(K_up, M, N);
+  if (st != MBOK_OK) return st;
+  if (group != MBOK_GROUP) return MBOK_ERR_UNSUPPORTED;
+  if (T < 1 || T > kMaxTokens) return MBOK_ERR_SHAPE;
+  if (packed_gate == nullptr || alpha_gate == nullptr || packed_up == nullptr || alpha_up == nullptr ||
+      X == nullptr || H == nullptr || (gate == nullptr) != (up == nullptr))
+    return MBOK_ERR_INVALID_ARG;
+  if (!aligned(packed_gate, 16) || !aligned(alpha_gate, 16) || !aligned(packed_up, 16) || !aligned(alpha_up, 16) ||
+      !aligned(X, 16) || !aligned(H, 16) || !aligned(gate, 16) || !aligned(up, 16))
+    return MBOK_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < gemm_gated_workspace_bytes(N, T) || !aligned(workspace, 256))
+    return MBOK_ERR_WORKSPACE;
+  return from_cuda(launch_gemm_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate,
+                                     make_shape(K_gate, M, N), reinterpret_cast<const uint8_t*>(packed_up), alpha_up,
+                                     make_shape(K_up, M, N), X, T, H, gate, up, workspace, as_stream(stream)));
+}
+
+size_t mbok_gemm_backward_workspace_bytes(int nseg, const int* K, const int* M, int N, int T) {
+  long long rows = 0;
+  if (check_multi(nseg, K, M, N, &rows) != MBOK_OK || T < 1 || T > kMaxTokens) return 0;
+  Shape shapes[8];
+  for (int i = 0; i < nseg; ++i) shapes[i] = make_shape(K[i], M[i], N);
+  return gemm_backward_workspace_bytes(nseg, shapes, T);
+}
+
+int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* const* alpha, const int* K,
+                       const int* M, int N, int group, const uint16_t* X, int T, const uint16_t* const* dY,
+                       uint16_t* dX, float* const* dalpha, void* workspace, size_t workspace_bytes, void* stream) {
+  long long rows = 0;
+  const int st = check_multi(nseg, K, M, N, &rows);
+  if (st != MBOK_OK) return st;
+  if (group != MBOK_GROUP) return MBOK_ERR_UNSUPPORTED;
+  if (T < 1 || T > kMaxTokens) return MBOK_ERR_SHAPE;
+  if (packed == nullptr || alpha == nullptr || dY == nullptr) return MBOK_ERR_INVALID_ARG;
+  Shape shapes[8];
+  const uint8_t* p8[8];
+  bool any = false;
+  for (int i = 0; i < nseg; ++i) {
+    if (packed[i] == nullptr || alpha[i] == nullptr || dY[i] == nullptr) return MBOK_ERR_INVALID_ARG;
+    if (!aligned(packed[i], 16) || !aligned(alpha[i], 16) || !aligned(dY[i], 16)) return MBOK_ERR_ALIGN;
+    if (dalpha != nullptr && dalpha[i] != nullptr) {
+      if (!aligned(dalpha[i], 16)) return MBOK_ERR_ALIGN;
+      any = true;
+    }
+    shapes[i] = make_shape(K[i], M[i], N);
+    p8[i] = reinterpret_cast<const uint8_t*>(packed[i]);
+  }
+  if (dX == nullptr && !any) return MBOK_ERR_INVALID_ARG;   // nothing asked for
+  if (any && X == nullptr) return MBOK_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(dX, 16)) return MBOK_ERR_ALIGN;
+  if (workspace == nullptr || workspace_bytes < gemm_backward_workspace_bytes(nseg, shapes, T) ||
+      !aligned(workspace, 256))
+    return MBOK_ERR_WORKSPACE;
+  return from_cuda(launch_gemm_backward(nseg, p8, alpha, shapes, X, T, dY, dX, dalpha, workspace, as_stream(stream)));
+}
+
 // Checks common to the distillation calls.
 static int check_distill(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
                          const int32_t* index, int top, float temperature) {
@@ -444,8 +518,10 @@ int mbok_read_device_errors(unsigned* flags) {
   const unsigned m = gemm_error_flags();
   const unsigned t = gemv_mma_error_flags();
   const unsigned d = gemv_gated_error_flags();
-  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u) return MBOK_ERR_CUDA;
-  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u);
+  const unsigned p = gemm_pair_error_flags();
+  const unsigned a = gemm_dalpha_error_flags();
+  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u || p == ~0u || a == ~0u) return MBOK_ERR_CUDA;
+  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u) | ((p | a) ? 8u : 0u);
   return MBOK_OK;
 }
 

@@ -292,6 +292,55 @@ int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int
                     const uint16_t* alpha_up, int K_up, int M, int N, int group, const void* x, int x_dtype, int batch,
                     void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace mbok_gemm_gated needs (256-byte aligned, no
+ * initialisation; calls that share one must not run concurrently): X scaled
+ * to fp16 and the tokens' scales.  0 on a bad argument. */
+size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T);
+
+/* The gated feed-forward block's first half for T tokens (prompts, training):
+ *     H[t][r] = silu(G) * U,   G[t][r] = sum_j W_gate[r][j] X[t][j],
+ *     U[t][r] = sum_j W_up[r][j] X[t][j],
+ * on the tensor cores, both projections and the gate in one kernel.
+ *   X        : bf16 [T][N].   H: out, bf16 [T][M].
+ *   gate, up : out, bf16 [T][M]: G and U for mbok_gated_backward, or both NULL.
+ *   All 16-byte aligned; 1 <= T <= 2^23.  Other arguments as mbok_gemv_gated.
+ *   workspace: mbok_gemm_gated_workspace_bytes(M, N, T) bytes.
+ * Each token's X is scaled by a power of two into fp16 (exact, but for values
+ * below 2^-29 of the token's largest, which are off by at most 2^-40 of it),
+ * each weight level rounded once to fp16 (relative 2^-11 for levels above
+ * 2^-12, absolute 2^-23 below), accumulation fp32, H computed from the fp32 G
+ * and U, every output rounded once: deterministic.  Waits inside the kernel
+ * are bounded: see mbok_read_device_errors (bit 3). */
+int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
+                    const uint16_t* alpha_up, int K_up, int M, int N, int group, const uint16_t* X, int T, uint16_t* H,
+                    uint16_t* gate, uint16_t* up, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace mbok_gemm_backward needs (256-byte aligned, no
+ * initialisation; calls that share one must not run concurrently).  0 on a
+ * bad argument. */
+size_t mbok_gemm_backward_workspace_bytes(int nseg, const int* K, const int* M, int N, int T);
+
+/* Backward pass of Boolean linear layers that share their input (one layer,
+ * gate and up, q/k/v): with Y_s = X W_s^T and dY_s = dL/dY_s,
+ *     dX[t][j]            = sum_s sum_r dY_s[t][r] W_s[r][j],
+ *     dalpha_s[k][r][g]   = sum_{j in group g} b_k[r][j] sum_t dY_s[t][r] X[t][j].
+ *   nseg, packed, alpha, K, M : as mbok_gemv_multi.
+ *   X      : bf16 [T][N] (may be NULL if no dalpha is asked for).
+ *   dY     : host array of device pointers, bf16 [T][M[s]].
+ *   dX     : out, bf16 [T][N], or NULL.
+ *   dalpha : host array of device pointers, out, fp32 in the layout of alpha
+ *            (mbok_alpha_elems(K[s], M[s], N) elements, pad rows 0), or NULL;
+ *            an entry may be NULL (a matrix whose scales are frozen).
+ *   All 16-byte aligned; 1 <= T <= 2^23.
+ * dX: dY scaled to fp16 per token (over all matrices), weight levels rounded
+ * once to fp16, as mbok_gemm_gated; one fp32 sum over all matrices, rounded
+ * once.  dalpha: products of the bf16 values are exact, sums fp32; the dense
+ * M x N gradient is never stored.  Deterministic.  Bounded waits: bit 3 of
+ * mbok_read_device_errors. */
+int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* const* alpha, const int* K,
+                       const int* M, int N, int group, const uint16_t* X, int T, const uint16_t* const* dY,
+                       uint16_t* dX, float* const* dalpha, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Gradient of the gate of mbok_gemm_gated: from dH = dL/dH and the two
  * projections that call kept,
  *     dgate = dH u s (1 + g (1 - s)),   dup = dH g s,   s = 1 / (1 + exp(-g)),
@@ -412,7 +461,8 @@ int mbok_gemv_noalloc(const uint32_t* packed, const uint16_t* alpha, int K, int 
  * Writes the flags accumulated on the current device since the last call to
  * *flags (0 = none; bit 0 = a whole-row lookup GEMV copy wait gave up, in
  * which case that CTA stored none of its rows of y; bit 1 = a prefill-GEMM
- * pipeline wait gave up; bit 2 = a tensor-core GEMV copy wait gave up, in
+ * pipeline wait gave up; bit 2 = a tensor-core GEMV copy wait gave up, bit 3 = a
+ * CTA-pair GEMM (mbok_gemm_gated, mbok_gemm_backward) pipeline wait gave up, in
  * which case that launch stored no outputs) and clears them.  Synchronises
  * the device.  Returns MBOK_ERR_CUDA if the flags cannot be read. */
 int mbok_read_device_errors(unsigned* flags);

@@ -287,3 +287,49 @@ def test_finetune_binding_refuses_cpu_tensors(L):
         mb.gated_backward(t, t, t, 1, 64, t, t)
     with pytest.raises(ValueError):
         mb.distill_loss(t, mb.BF16, 1, 64, 64, t, t, 1, 1.0, None, t, t)
+
+
+def test_gemm_gated_sizes_and_argument_errors(L):
+    up = lambda n, m: (n + m - 1) // m * m
+    assert L.mbok_gemm_gated_workspace_bytes(100, 256, 33) == up(33 * 256 * 2, 256) + up(33, 16) * 4
+    assert L.mbok_gemm_gated_workspace_bytes(100, 250, 33) == 0 and L.mbok_gemm_gated_workspace_bytes(100, 256, 0) == 0
+    g = lambda **kw: L.mbok_gemm_gated(*[kw.get(k, v) for k, v in dict(
+        pg=FAKE, ag=FAKE, Kg=3, pu=FAKE, au=FAKE, Ku=2, M=64, N=1024, group=128, X=FAKE, T=40, H=FAKE, gate=None,
+        up=None, ws=FAKE, wsb=1 << 24, stream=None).items()])
+    assert g(Kg=0) == 1 and g(Ku=5) == 1 and g(M=0) == 2 and g(N=100) == 2 and g(group=64) == 4
+    assert g(T=0) == 2 and g(T=(1 << 23) + 1) == 2
+    for name in ("pg", "ag", "pu", "au", "X", "H"):
+        assert g(**{name: None}) == 1 and g(**{name: FAKE + 8}) == 3
+    assert g(gate=FAKE) == 1 and g(up=FAKE) == 1                    # both projections or neither
+    assert g(gate=FAKE + 2, up=FAKE) == 3 and g(gate=FAKE, up=FAKE + 8) == 3
+    assert g(ws=None) == 6 and g(wsb=16) == 6 and g(ws=FAKE + 16) == 6
+
+
+def test_gemm_backward_sizes_and_argument_errors(L):
+    import boolean_weight_matmul_b200 as mb
+    one = mb.gemm_backward_workspace_bytes([3], [64], 1024, 40)
+    ragged = mb.gemm_backward_workspace_bytes([3], [63], 1024, 40)
+    assert one >= 40 * 64 * 2 + 48 * 4 and ragged >= one + 40 * 64 * 2     # the copy with aligned rows
+    # few tiles and many tokens: partial sums of several token splits
+    assert mb.gemm_backward_workspace_bytes([1], [64], 256, 4096) > 4096 * 64 * 2 + 2 * 64 * 2 * 4
+    assert mb.gemm_backward_workspace_bytes([5], [64], 1024, 40) == 0
+    assert mb.gemm_backward_workspace_bytes([1] * 9, [8] * 9, 1024, 40) == 0
+    assert mb.gemm_backward_workspace_bytes([1], [8], 1000, 40) == 0
+    assert mb.gemm_backward_workspace_bytes([1], [8], 1024, 0) == 0
+
+    arr = lambda *v: ctypes.cast((ctypes.c_void_p * len(v))(*v), ctypes.c_void_p)
+    ia = lambda *v: ctypes.cast((ctypes.c_int * len(v))(*v), ctypes.c_void_p)
+    g = lambda **kw: L.mbok_gemm_backward(*[kw.get(k, v) for k, v in dict(
+        n=2, packed=arr(FAKE, FAKE), alpha=arr(FAKE, FAKE), K=ia(3, 2), M=ia(64, 40), N=1024, group=128, X=FAKE, T=40,
+        dY=arr(FAKE, FAKE), dX=FAKE, da=arr(FAKE, FAKE), ws=FAKE, wsb=1 << 26, stream=None).items()])
+    assert g(n=0) == 1 and g(n=9) == 1 and g(K=None) == 1 and g(M=None) == 1
+    assert g(K=ia(3, 5)) == 1 and g(M=ia(64, 0)) == 2 and g(N=1000) == 2 and g(group=64) == 4
+    assert g(T=0) == 2 and g(T=(1 << 23) + 1) == 2
+    for name in ("packed", "alpha", "dY"):
+        assert g(**{name: None}) == 1 and g(**{name: arr(FAKE, None)}) == 1 and g(**{name: arr(FAKE, FAKE + 8)}) == 3
+    assert g(da=arr(None, FAKE + 8)) == 3 and g(dX=FAKE + 8) == 3 and g(X=FAKE + 8) == 3
+    assert g(dX=None, da=None) == 1 and g(dX=None, da=arr(None, None)) == 1       # nothing asked for
+    assert g(X=None) == 1                                                          # scales need X
+    assert g(ws=None) == 6 and g(wsb=16) == 6 and g(ws=FAKE + 16) == 6
+    with pytest.raises(ValueError):
+        mb.gemm_backward([FAKE], [FAKE, FAKE], [1], [8], 128, 128, FAKE, 1, [FAKE], FAKE, None, None)

@@ -388,3 +388,316 @@ def test_distill_gradient_against_differences():
         args = (teacher.astype(np.float64), index, tau, weight.astype(np.float64), one)
         d = (F.distill(hi, *args)[0] - F.distill(lo, *args)[0]) / (2 * eps)
         _assert_within(_f64(dz[:, j]), d, 1e-6)
+
+
+# ---- gated feed-forward over tokens ---------------------------------------------
+
+def _dense_abs(layer):
+    a = np.repeat(layer.alpha.astype(np.float64), 128, axis=1)
+    return np.einsum("mnk,kmn->mn", a, F.planes(layer.words, layer.K, layer.M, layer.N))
+
+
+def _fp16_weights_tol(absx, W, n):
+    # Each level is rounded once to fp16: half a step 2^-11 of it, or 2^-23 where
+    # it is below 2^-12.  The tensor cores add 16 products at a time into an fp32
+    # sum that they may truncate: a full step 2^-23 per addition, n / 16 + 16 deep.
+    # Scaled activations are off by at most 2^-40 of their token's largest.
+    E = absx @ np.abs(W).T
+    return E * (2.0 ** -11 + (n / 16 + 16) * 2.0 ** -23) + absx.sum(1, keepdims=True) * 2.0 ** -23 + \
+        absx.max(1, keepdims=True) * 2.0 ** -40 * np.abs(W).sum(1)[None, :]
+
+
+def _gemm_gated(gate, up, X, keep, ws=None):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T = X.shape[0]
+    out = [guarded((T, gate.M), torch.bfloat16) for _ in range(3)]
+    if ws is None:
+        ws = mb.empty_gemm_gated_workspace(gate.M, gate.N, T)
+        ws.fill_(0xFF)
+    mb.gemm_gated(gate.packed, gate.blocked, gate.K, up.packed, up.blocked, up.K, gate.M, gate.N, 128, X, T, out[0],
+                  out[1] if keep else None, out[2] if keep else None, ws)
+    torch.cuda.synchronize()
+    assert mb.read_device_errors() == 0
+    return out
+
+
+def _check_gated(gate, up, x64, got, keep):
+    Wg, Wu, ax = _dense_abs(gate), _dense_abs(up), np.abs(x64)
+    g, u = x64 @ Wg.T, x64 @ Wu.T
+    tg, tu = _fp16_weights_tol(ax, Wg, gate.N), _fp16_weights_tol(ax, Wu, gate.N)
+    h = F.silu(g) * u
+    # bf16's smallest value is 2^-133: a result near or below it is off by up to half of that, 2^-134, whatever
+    # its relative bound (the products of two 1e-30 tokens are 1e-64 and come out as 0)
+    tg, tu = tg + 2.0 ** -134, tu + 2.0 ** -134
+    th = 1.01 * (1.1 * np.abs(u) * tg + np.abs(F.silu(g)) * tu + 1.1 * tg * tu) + \
+        np.abs(h) * (2.0 ** -20 + np.abs(g) * 2.0 ** -23 + HALF["bf16"]) + 2.0 ** -134
+    _assert_within(_f64(got[0]), h, th, "H")
+    if keep:
+        _assert_within(_f64(got[1]), g, tg + np.abs(g) * HALF["bf16"], "gate")
+        _assert_within(_f64(got[2]), u, tu + np.abs(u) * HALF["bf16"], "up")
+
+
+@pytest.mark.parametrize("kg,ku", [(1, 1), (2, 4), (3, 3), (4, 1)])
+@pytest.mark.parametrize("M,N,T", [(128, 128, 32), (1, 128, 1), (7, 256, 17), (200, 640, 77), (1001, 384, 130),
+                                   (64, 2048, 300), (136, 128, 700)])
+def test_gemm_gated(kg, ku, M, N, T):
+    gate, up = Layer(kg, M, N, 500 + kg + M, pad_nan=True), Layer(ku, M, N, 600 + ku + N, pad_nan=True)
+    x, x64 = _x(T, N, 700 + T, "bf16")
+    for keep in (True, False):
+        _check_gated(gate, up, x64, _gemm_gated(gate, up, x_dev(x, "bf16"), keep), keep)
+
+
+def test_gemm_gated_many_tiles():
+    # more tiles than pairs of CTAs: every pair reuses its accumulators
+    gate, up = Layer(3, 1500, 256, 31), Layer(2, 1500, 256, 32)
+    x, x64 = _x(4100, 256, 33, "bf16")
+    _check_gated(gate, up, x64, _gemm_gated(gate, up, x_dev(x, "bf16"), True), True)
+
+
+def test_gemm_gated_activation_range():
+    # tokens of very different size, zeros, subnormals, infinities and NaN: a token's scale is its own
+    import torch
+    gate, up = Layer(2, 40, 256, 41), Layer(1, 40, 256, 42)
+    rng = np.random.default_rng(43)
+    x = rng.standard_normal((12, 256))
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    x[2] = 0
+    x[3] *= 2.0 ** -130
+    x[4, 3], x[5, 7], x[6, 9] = np.inf, -np.inf, np.nan
+    x[7, ::2] *= 1e-6
+    X = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    x64 = _f64(X)
+    got = _gemm_gated(gate, up, X, True)
+    finite = [t for t in range(12) if t not in (0, 4, 5, 6)]
+    _check_gated(gate, up, x64[finite], [o[finite] for o in got], True)
+    # the large token's projections (their product overflows)
+    Wg, Wu = _dense_abs(gate), _dense_abs(up)
+    for o, W in ((got[1], Wg), (got[2], Wu)):
+        _assert_within(_f64(o[:1]), x64[:1] @ W.T, _fp16_weights_tol(np.abs(x64[:1]), W, 256) +
+                       np.abs(x64[:1] @ W.T) * HALF["bf16"])
+    assert not torch.isfinite(got[1][4]).any() and not torch.isfinite(got[1][5]).any() and torch.isnan(got[1][6]).all()
+
+
+# ---- backward pass of layers that share X ---------------------------------------
+
+def _unblock(a, K, M, N):
+    """fp32 [M][G][K] from the scales' layout [octet][group][kernel][8]."""
+    return a.reshape(-1, N // 128, K, 8).transpose(0, 3, 1, 2).reshape(-1, N // 128, K)[:M]
+
+
+def _grads(T, M, seed, scale=1e-2):
+    import torch
+    rng = np.random.default_rng(seed)
+    return torch.from_numpy(rng.standard_normal((T, M)) * scale).to(torch.bfloat16).cuda()
+
+
+def _gemm_backward(layers, X, dYs, want_x=True, want_a=None, ws=None):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, N = X.shape
+    Ks, Ms = [m.K for m in layers], [m.M for m in layers]
+    want_a = [True] * len(layers) if want_a is None else want_a
+    dX = guarded((T, N), torch.bfloat16) if want_x else None
+    das = [guarded((mb.alpha_elems(m.K, m.M, N),), torch.float32) if w else None for m, w in zip(layers, want_a)]
+    if ws is None:
+        ws = mb.empty_gemm_backward_workspace(Ks, Ms, N, T)
+        ws.fill_(0xFF)
+    mb.gemm_backward([m.packed for m in layers], [m.blocked for m in layers], Ks, Ms, N, 128, X, T, dYs, dX, das, ws)
+    torch.cuda.synchronize()
+    assert mb.read_device_errors() == 0
+    return dX, das
+
+
+def _check_backward(layers, X, dYs, dX, das):
+    N, T = X.shape[1], X.shape[0]
+    x64, dy64 = _f64(X), [_f64(d) for d in dYs]
+    want, _, wa = F.layer_grad([m.host() for m in layers], N, x64, dy64)
+    if dX is not None:
+        tol = np.abs(want) * HALF["bf16"]
+        rows = sum(m.M for m in layers)
+        top = np.max([np.abs(d).max(1) for d in dy64], axis=0)[:, None]   # one scale per token
+        for m, d in zip(layers, dy64):
+            W = _dense_abs(m)
+            E = np.abs(d) @ np.abs(W)
+            tol = tol + E * (2.0 ** -11 + (rows / 16 + 16 * len(layers) + 16) * 2.0 ** -23) + \
+                np.abs(d).sum(1, keepdims=True) * 2.0 ** -23 + top * 2.0 ** -40 * np.abs(W).sum(0)[None, :]
+        _assert_within(_f64(dX), want, tol, "dX")
+    for m, da, (w, E) in zip(layers, das, wa):
+        if da is None:
+            continue
+        blocked = da.cpu().numpy()
+        got = _unblock(blocked, m.K, m.M, N)
+        # exact products; at most 64 tensor-core steps a run, then 32 + 8 fp32 additions and one per run or split
+        tol = E * (min(T, 1024) / 16 + 16) * 2.0 ** -23 + E * (48 + T / 256) * 2.0 ** -24
+        _assert_within(got, w, tol, "dalpha")
+        pad = blocked.reshape(-1, N // 128, m.K, 8)[-1, :, :, m.M % 8:] if m.M % 8 else np.zeros(1)
+        assert (pad == 0).all()
+
+
+@pytest.mark.parametrize("spec", [[(1, 1)], [(3, 7)], [(2, 64)], [(4, 200)], [(3, 136), (2, 77)],
+                                  [(2, 200), (1, 77), (3, 77)], [(1, 8), (2, 9), (3, 65), (4, 130), (1, 300), (2, 1),
+                                                                 (3, 64), (4, 15)]])
+@pytest.mark.parametrize("N,T", [(128, 1), (256, 33), (640, 130)])
+def test_gemm_backward(spec, N, T):
+    layers = [Layer(K, M, N, 50 + 7 * i + M, pad_nan=True) for i, (K, M) in enumerate(spec)]
+    X = x_dev(wl.x_normal(T, N, 60 + T), "bf16")
+    dYs = [_grads(T, m.M, 70 + i) for i, m in enumerate(layers)]
+    dX, das = _gemm_backward(layers, X, dYs)
+    _check_backward(layers, X, dYs, dX, das)
+
+
+@pytest.mark.parametrize("M,N,T", [(300, 384, 2500), (1500, 1280, 300), (513, 2304, 1100)])
+def test_gemm_backward_runs_splits_and_tiles(M, N, T):
+    # several token runs, token splits, more tiles than pairs
+    layers = [Layer(3, M, N, 81), Layer(2, 40, N, 82)]
+    X = x_dev(wl.x_normal(T, N, 83), "bf16")
+    dYs = [_grads(T, m.M, 84 + i) for i, m in enumerate(layers)]
+    first = _gemm_backward(layers, X, dYs)
+    _check_backward(layers, X, dYs, *first)
+    import torch
+    again = _gemm_backward(layers, X, dYs)
+    assert torch.equal(first[0], again[0]) and all(torch.equal(a, b) for a, b in zip(first[1], again[1]))
+
+
+def test_gemm_backward_parts():
+    # dX alone (no X needed), scales alone, one matrix's scales frozen: the same bits as all together
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    N, T = 512, 90
+    layers = [Layer(2, 100, N, 91), Layer(3, 64, N, 92)]
+    X = x_dev(wl.x_normal(T, N, 93), "bf16")
+    dYs = [_grads(T, m.M, 94 + i) for i, m in enumerate(layers)]
+    dX, das = _gemm_backward(layers, X, dYs)
+    only_a = _gemm_backward(layers, X, dYs, want_x=False)
+    frozen = _gemm_backward(layers, X, dYs, want_a=[False, True])
+    assert all(torch.equal(a, b) for a, b in zip(das, only_a[1]))
+    assert torch.equal(frozen[0], dX) and torch.equal(frozen[1][1], das[1])
+    alone = guarded((T, N), torch.bfloat16)
+    ws = mb.empty_gemm_backward_workspace([2, 3], [100, 64], N, T)
+    mb.gemm_backward([m.packed for m in layers], [m.blocked for m in layers], [2, 3], [100, 64], N, 128, None, T, dYs,
+                     alone, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(alone, dX)
+
+
+def test_gemm_backward_range():
+    # gradients far below and above one, zero rows, an infinity and a NaN that stay in their token
+    import torch
+    N, T = 256, 20
+    layers = [Layer(3, 72, N, 101)]
+    X = x_dev(wl.x_normal(T, N, 102), "bf16")
+    d = _grads(T, 72, 103)
+    d[0] *= 1e-30
+    d[1] *= 1e30
+    d[2] = 0
+    clean = d.clone()
+    d[3, 5], d[4, 6] = float("inf"), float("nan")
+    dX, _ = _gemm_backward(layers, X, [d], want_a=[False])
+    keep = [t for t in range(T) if t not in (3, 4)]
+    _check_backward(layers, X[keep].contiguous(), [clean[keep].contiguous()], dX[keep], [None])
+    assert not torch.isfinite(dX[3]).any() and torch.isnan(dX[4]).all()
+
+
+def test_gemm_backward_against_differences():
+    # the scales' gradient by the definition: move one scale, take the difference of sum(dY * Y)
+    K, M, N, T = 2, 16, 256, 40
+    layer = Layer(K, M, N, 111)
+    X = x_dev(wl.x_normal(T, N, 112), "bf16")
+    dY = _grads(T, M, 113)
+    _, (da,) = _gemm_backward([layer], X, [dY])
+    got = _unblock(da.cpu().numpy(), K, M, N)
+    x64, d64 = _f64(X), _f64(dY)
+    for r, g, k in ((0, 0, 0), (5, 1, 1), (15, 0, 1)):
+        vals = []
+        for sign in (1, -1):
+            a = layer.alpha.astype(np.float64).copy()
+            a[r, g, k] += sign * 1e-3
+            vals.append((d64 * F.project(layer.words, a, K, M, N, x64)[0]).sum())
+        want = (vals[0] - vals[1]) / 2e-3
+        assert abs(got[r, g, k] - want) <= 1e-4 * max(1.0, abs(want))
+
+
+# ---- a run of them together -------------------------------------------------------
+
+def test_block_training_step():
+    # gated block -> down projection -> output layer -> distillation, and back to every scale and the input
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, D, M, V, top, tau = 48, 256, 384, 640, 8, 2.0
+    gate, up, down, head = Layer(2, M, D, 121), Layer(3, M, D, 122), Layer(2, D, M, 123), Layer(3, V, D, 124)
+    x, x64 = _x(T, D, 125, "bf16")
+    X = x_dev(x, "bf16")
+    H, G, U = _gemm_gated(gate, up, X, True)
+    Y = guarded((T, D), torch.bfloat16)
+    mb.gemm(down.packed, down.blocked, down.K, D, M, 128, H, T, Y, precision=mb.GEMM_SPLIT)
+    Z = guarded((T, V), torch.bfloat16)
+    mb.gemm(head.packed, head.blocked, head.K, V, D, 128, Y, T, Z, precision=mb.GEMM_SPLIT)
+    _, teacher, index, weight, _ = _distill_case(T, V, top, 126, "bf16")
+    loss, lse, dZ = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), torch.bfloat16)
+    mb.distill_loss(Z, mb.BF16, T, V, V, to_dev(teacher), to_dev(index), top, tau, to_dev(weight), loss, lse, dZ, V)
+    torch.cuda.synchronize()
+    dY, (da_head,) = _gemm_backward([head], Y, [dZ])
+    dH, (da_down,) = _gemm_backward([down], H, [dY])
+    dG, dU, H2 = (guarded((T, M), torch.bfloat16) for _ in range(3))
+    mb.gated_backward(dH, G, U, T, M, dG, dU, H2)
+    dX, (da_gate, da_up) = _gemm_backward([gate, up], X, [dG, dU])
+    torch.cuda.synchronize()
+    # the same step in fp64 from the same inputs: every bf16 rounding on the way adds its half step, about
+    # sqrt(8) x 2^-8 of a result's size after eight of them
+    f = lambda layer, a: a @ _dense_abs(layer).T
+    g, u = f(gate, x64), f(up, x64)
+    h = F.silu(g) * u
+    y = f(down, h)
+    z = f(head, y)
+    _, _, dz, _, _ = F.distill(z, teacher.astype(np.float64), index, tau, weight.astype(np.float64), np.ones(T))
+    dy, _, ((a_head, _),) = F.layer_grad([head.host()], D, y, [dz])
+    dh, _, ((a_down, _),) = F.layer_grad([down.host()], M, h, [dy])
+    dg, du, _, _ = F.gated_grad(dh, g, u)
+    dx, _, ((a_gate, _), (a_up, _)) = F.layer_grad([gate.host(), up.host()], D, x64, [dg, du])
+    rel = lambda got, want: np.linalg.norm(got - want) / np.linalg.norm(want)
+    for name, got, want in (("dX", _f64(dX), dx),
+                            ("head", _unblock(da_head.cpu().numpy(), 3, V, D), a_head),
+                            ("down", _unblock(da_down.cpu().numpy(), 2, D, M), a_down),
+                            ("gate", _unblock(da_gate.cpu().numpy(), 2, M, D), a_gate),
+                            ("up", _unblock(da_up.cpu().numpy(), 3, M, D), a_up)):
+        assert rel(got, want) <= 8 ** 0.5 * 2.0 ** -8, (name, rel(got, want))
+
+
+def test_gemm_calls_captured_and_on_another_stream():
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    gate, up = Layer(3, 200, 512, 131), Layer(2, 200, 512, 132)
+    T = 70
+    X = x_dev(wl.x_normal(T, 512, 133), "bf16")
+    want = [t.clone() for t in _gemm_gated(gate, up, X, True)]
+    dYs = [_grads(T, 200, 134), _grads(T, 200, 135)]
+    bwd = _gemm_backward([gate, up], X, dYs)
+    ws, wb = mb.empty_gemm_gated_workspace(200, 512, T), mb.empty_gemm_backward_workspace([3, 2], [200, 200], 512, T)
+    out = [torch.zeros_like(t) for t in want]
+    dX, das = torch.zeros_like(bwd[0]), [torch.zeros_like(a) for a in bwd[1]]
+
+    def calls():
+        mb.gemm_gated(gate.packed, gate.blocked, 3, up.packed, up.blocked, 2, 200, 512, 128, X, T, *out, ws)
+        mb.gemm_backward([gate.packed, up.packed], [gate.blocked, up.blocked], [3, 2], [200, 200], 512, 128, X, T, dYs,
+                         dX, das, wb)
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert torch.equal(dX, bwd[0]) and all(torch.equal(a, b) for a, b in zip(das, bwd[1]))
+        for t in (*out, dX, *das):
+            t.zero_()
+        torch.cuda.synchronize()
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        calls()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(2):
+        graph.replay()
+        check()
