@@ -25,9 +25,12 @@
 //    are a 128-byte line with one k, the M-major form of the same swizzled
 //    layout, so the unpack is the same and nothing is transposed.
 //
-// Per stage: TMA brings the tile's bits and scales and this CTA's half of the
-// tokens onto one barrier; 16 unpack warps write A and arrive on the leader's
-// `ready` barrier; the leader's MMA thread issues 4 x (1 or 2) tcgen05.mma
+// Per stage: TMA brings this CTA's half of the tokens, completing on the
+// leader's barrier, and the tile's bits and scales, in a ring of their own that
+// runs ahead; four unpack warps write A and arrive on the leader's `ready`
+// barrier (16 unpack warps in four groups, one per ring slot: with all 16 on
+// every stage the latency of wait, load, store, fence and arrival bounded each
+// stage at about 1 us, whatever the tokens); the leader's MMA thread issues 4 x (1 or 2) tcgen05.mma
 // (M = 256, N <= 256, K = 16) and commits the stage to both CTAs' `empty`
 // barriers.  The unpack warps also drain the accumulator (up to 512 columns,
 // all of tensor memory) after a tile's last stage: 16 warps, four per lane
@@ -49,12 +52,16 @@ constexpr int kPairOctets = 8;                                // row octets of a
 constexpr int kPairBits = 2 * kPairOctets * MBOK_MAX_K * 64;  // 4 KB: GATE two boxes of 64 bytes, GRAD one of 128
 constexpr int kPairAlpha = 2 * kPairOctets * MBOK_MAX_K * 16; // 1 KB
 constexpr int kPairAOff = 2 * kPairXBytes;
-constexpr int kPairBitsOff = kPairAOff + kPairABytes;
-constexpr int kPairAlphaOff = kPairBitsOff + kPairBits;
-constexpr int kPairStageBytes = kPairAlphaOff + kPairAlpha;   // 53 KB
-constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024 + 256;
+constexpr int kPairStageBytes = kPairAOff + kPairABytes;      // 48 KB: tokens and A
+constexpr int kPairWStages = 6;                               // a deeper ring for the bits and scales
+constexpr int kPairWBytes = kPairBits + kPairAlpha;           // 5 KB
+constexpr int kPairWOff = kPairStages * kPairStageBytes;
+constexpr int kPairBarOff = kPairWOff + kPairWStages * kPairWBytes;
+constexpr int kPairSmem = kPairBarOff + 1024 + 256;
 constexpr int kPairUnpackWarps = 16;
-constexpr int kPairThreads = (2 + kPairUnpackWarps) * 32;
+constexpr int kPairGroupWarps = kPairUnpackWarps / kPairStages;   // unpack warps per ring slot
+constexpr int kPairUnpackWarp0 = 3;                               // after the two copy warps and the MMA warp
+constexpr int kPairThreads = (kPairUnpackWarp0 + kPairUnpackWarps) * 32;
 constexpr unsigned kPairTmemCols = 512;
 
 static __device__ unsigned int g_pair_error;
@@ -86,45 +93,51 @@ struct PairParams {
   uint16_t* up;
 };
 
-// One row x 16 columns of K kernels: 16-bit halves of the row's bits at `src`
-// (kernel k at src + k * kstride) to two swizzled 16-byte chunks of `line`.
+// Four units (64 columns) of one row: the row's bits of kernel k and unit u at
+// src + k * kstride + u * 16, to the eight swizzled 16-byte chunks of `line`.
+// Units are taken in the order u ^ flip.
 template <int K>
 __device__ __forceinline__ void pair_unpack(const unsigned char* src, int kstride, const uint32_t P[4],
-                                            unsigned char* line, int unit, int r) {
-  uint32_t h[K], out[8];
+                                            unsigned char* line, int r, int flip) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) h[k] = *reinterpret_cast<const uint16_t*>(src + k * kstride);
-  tc_unpack_row<K>(h, P, out);
-  const int c0 = (2 * unit) ^ (r & 7), c1 = (2 * unit + 1) ^ (r & 7);
-  *reinterpret_cast<uint4*>(line + c0 * 16) = make_uint4(out[0], out[1], out[2], out[3]);
-  *reinterpret_cast<uint4*>(line + c1 * 16) = make_uint4(out[4], out[5], out[6], out[7]);
+  for (int n = 0; n < 4; ++n) {
+    const int u = n ^ flip;
+    uint32_t h[K], out[8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) h[k] = *reinterpret_cast<const uint16_t*>(src + k * kstride + u * 16);
+    tc_unpack_row<K>(h, P, out);
+    const int c0 = (2 * u) ^ (r & 7), c1 = (2 * u + 1) ^ (r & 7);
+    *reinterpret_cast<uint4*>(line + c0 * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(line + c1 * 16) = make_uint4(out[4], out[5], out[6], out[7]);
+  }
 }
 
-// GATE: thread tid unpacks unit tid & 3 of A row tid >> 2.  A row 32 q + l is
-// row 16 q + (l & 15) of the gate (l < 16) or up matrix's 64 rows of this tile.
-// The levels P are formed on the first of a 128-column group's two stages.
+// GATE: thread gt of a group's 128 unpacks one A row's 64 columns; threads
+// 0..63 the gate matrix's rows of this tile, 64..127 the up matrix's.  Row m of
+// a matrix is A row 32 (m / 16) + m % 16, + 16 for up.  Eight lanes that store
+// together hold eight consecutive rows: distinct chunks.
 template <int K>
-__device__ __forceinline__ void unpack_gate(const unsigned char* st, unsigned char* a, int tid, bool is_up, bool first,
-                                            uint32_t P[4]) {
-  const int r = tid >> 2, u = tid & 3;
-  const int o = 2 * (r >> 5) + ((r >> 3) & 1), i = r & 7;
-  const unsigned char* bits = st + kPairBitsOff + (is_up ? kPairBits / 2 : 0);
-  const unsigned char* alpha = st + kPairAlphaOff + (is_up ? kPairAlpha / 2 : 0);
-  if (first) tc_levels_f16<K>(alpha, o, i, false, P);
-  pair_unpack<K>(bits + (o * K * 4 + u) * 16 + 2 * i, 64, P, a + r * 128, u, r);
+__device__ __forceinline__ void unpack_gate(const unsigned char* w, unsigned char* a, int gt) {
+  const int up = gt >> 6, m = gt & 63;
+  const int o = m >> 3, i = m & 7;
+  const int r = 32 * (m >> 4) + 16 * up + (m & 15);
+  uint32_t P[4];
+  tc_levels_f16<K>(w + kPairBits + up * (kPairAlpha / 2), o, i, false, P);
+  pair_unpack<K>(w + up * (kPairBits / 2) + o * K * 64 + 2 * i, 64, P, a + r * 128, r, 0);
 }
 
-// GRAD: one unit of one of the stage's 64 rows per thread (128 columns, one
-// group, in two blocks of 64); the 8 threads of a store phase write two rows'
-// four units of one block, 8 distinct chunks.  Rows at or beyond M are zeros:
+// GRAD: thread gt of a group's 128 unpacks block gt & 1 (64 columns) of row
+// gt >> 1 of the stage's 64 rows.  Eight lanes that store together hold four
+// rows of both blocks; the second block's units go in the order 2, 3, 0, 1, so
+// that its chunks differ from the first's.  Rows at or beyond M are zeros:
 // their stored scales mean nothing and could be NaN.
 template <int K>
-__device__ __forceinline__ void unpack_grad(const unsigned char* st, unsigned char* a, int tid, int rows) {
-  const int r = 2 * (tid >> 4) + ((tid >> 2) & 1), u = (tid & 3) + ((tid >> 1) & 4);
+__device__ __forceinline__ void unpack_grad(const unsigned char* w, unsigned char* a, int gt, int rows) {
+  const int r = gt >> 1, b = gt & 1;
   const int o = r >> 3, i = r & 7;
   uint32_t P[4];
-  tc_levels_f16<K>(st + kPairAlphaOff, o, i, r >= rows, P);
-  pair_unpack<K>(st + kPairBitsOff + (o * K * 8 + u) * 16 + 2 * i, 128, P, a + (u >> 2) * 8192 + r * 128, u & 3, r);
+  tc_levels_f16<K>(w + kPairBits, o, i, r >= rows, P);
+  pair_unpack<K>(w + o * K * 128 + b * 64 + 2 * i, 128, P, a + b * 8192 + r * 128, r, 2 * b);
 }
 
 // 16 accumulator columns of this warp's 32 lanes.
@@ -223,11 +236,13 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);   // this CTA's copies landed
-  uint64_t* empty = full + kPairStages;    // the stage's MMAs are done (both CTAs)
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(smem + kPairBarOff);   // bits and scales landed
+  uint64_t* wempty = wfull + kPairWStages; // ... and unpacked
+  uint64_t* xfull = wempty + kPairWStages; // leader: both CTAs' tokens landed
+  uint64_t* ready = xfull + kPairStages;   // leader: both CTAs' A is unpacked
+  uint64_t* empty = ready + kPairStages;   // the stage's MMAs are done (both CTAs)
   uint64_t* tfull = empty + kPairStages;   // the accumulator holds a finished tile (both CTAs)
-  uint64_t* ready = tfull + 1;             // leader: both CTAs' A is unpacked and their tokens landed
-  uint64_t* tempty = ready + kPairStages;  // leader: both CTAs drained the accumulator
+  uint64_t* tempty = tfull + 1;            // leader: both CTAs drained the accumulator
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
   __shared__ int s_fail;
 
@@ -236,10 +251,14 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairWStages; ++s) {
+      tc_mbar_init(&wfull[s], 1);
+      tc_mbar_init(&wempty[s], kPairGroupWarps);
+    }
     for (int s = 0; s < kPairStages; ++s) {
-      tc_mbar_init(&full[s], 1);
+      tc_mbar_init(&xfull[s], 1);
+      tc_mbar_init(&ready[s], 2 * kPairGroupWarps);
       tc_mbar_init(&empty[s], 1);
-      tc_mbar_init(&ready[s], 2 * kPairUnpackWarps);
     }
     tc_mbar_init(tfull, 1);
     tc_mbar_init(tempty, 2 * kPairUnpackWarps);
@@ -256,111 +275,142 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   bool ok = true;
 
   if (warp == 0) {
-    // ---- TMA producer ----
-    if (lane == 0) {
-      const int n_half = p.n_acc / 2;
-      int g = 0;
-      for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
-        const int rt = tile % p.row_tiles;
-        const int t0 = (tile / p.row_tiles) * (p.n_acc * p.naccs) + rank * n_half;
-        int m = 0, step = 0;   // GRAD: matrix and its 64-row step
-        for (int kb = 0; kb < p.stages; ++kb, ++g) {
-          const int s = g % kPairStages;
-          if (g >= kPairStages && !pair_wait(&empty[s], unsigned((g / kPairStages) - 1) & 1u)) { ok = false; break; }
-          unsigned char* st = smem + s * kPairStageBytes;
-          const unsigned act_bytes = unsigned(p.naccs * n_half * kPairBK * 2);
-          if (MODE == kGate) {
-            const int o = (rt * 128 + rank * 64) / kOctet;
-            tc_arrive_expect_tx(&full[s],
-                                act_bytes + unsigned(p.mat[0].K + p.mat[1].K) * kPairOctets * (64 + 16));
+    // ---- token copies ----
+    const int n_half = p.n_acc / 2;
+    const unsigned bytes = unsigned(2 * p.naccs * n_half * kPairBK * 2);   // both CTAs'
+    int g = 0;
+    for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
+      const int t0 = (tile / p.row_tiles) * (p.n_acc * p.naccs) + rank * n_half;
+      int m = 0, step = 0;   // GRAD: matrix and its 64-row step
+      for (int kb = 0; kb < p.stages; ++kb, ++g) {
+        const int s = g % kPairStages;
+        if (g >= kPairStages && !pair_wait(&empty[s], unsigned((g / kPairStages) - 1) & 1u)) { ok = false; break; }
+        unsigned char* st = smem + s * kPairStageBytes;
+        const uint32_t bar = pair_leader(&xfull[s]);
+        const CUtensorMap* map = &maps.act[MODE == kGate ? 0 : m];
+        const int x = (MODE == kGate ? kb : step) * kPairBK;
+        if (elect_lane()) {
+          if (rank == 0) tc_arrive_expect_tx(&xfull[s], bytes);
+          pair_tma_load_2d(st, map, x, t0, bar);
+          if (p.naccs > 1) pair_tma_load_2d(st + kPairXBytes, map, x, t0 + p.n_acc, bar);
+        }
+        __syncwarp();
+        if (MODE == kGrad && ++step == p.mat[m].stages) { step = 0; ++m; }
+      }
+    }
+  } else if (warp == 2) {
+    // ---- copies of bits and scales ----
+    int g = 0;
+    for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
+      const int rt = tile % p.row_tiles;
+      int m = 0, step = 0;
+      for (int kb = 0; kb < p.stages; ++kb, ++g) {
+        const int s = g % kPairWStages;
+        if (g >= kPairWStages && !pair_wait(&wempty[s], unsigned((g / kPairWStages) - 1) & 1u)) { ok = false; break; }
+        unsigned char* w = smem + kPairWOff + s * kPairWBytes;
+        if (MODE == kGate) {
+          const int o = (rt * 128 + rank * 64) / kOctet;
+          if (elect_lane()) {
+            tc_arrive_expect_tx(&wfull[s], unsigned(p.mat[0].K + p.mat[1].K) * kPairOctets * (64 + 16));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int K = p.mat[i].K;
-              tc_tma_load_2d(st + kPairBitsOff + i * (kPairBits / 2), &maps.bits[i], kb * 64, o * K, &full[s]);
-              tc_tma_load_2d(st + kPairAlphaOff + i * (kPairAlpha / 2), &maps.alpha[i], (kb / 2) * K * kOctet, o,
-                             &full[s]);
+              tc_tma_load_2d(w + i * (kPairBits / 2), &maps.bits[i], kb * 64, o * K, &wfull[s]);
+              tc_tma_load_2d(w + kPairBits + i * (kPairAlpha / 2), &maps.alpha[i], (kb / 2) * K * kOctet, o, &wfull[s]);
             }
-            for (int a = 0; a < p.naccs; ++a)
-              tc_tma_load_2d(st + a * kPairXBytes, &maps.act[0], kb * kPairBK, t0 + a * p.n_acc, &full[s]);
-          } else {
-            const int K = p.mat[m].K;
-            const int j = rt * 256 + rank * 128;
-            tc_arrive_expect_tx(&full[s], act_bytes + unsigned(K) * kPairOctets * (128 + 16));
-            tc_tma_load_2d(st + kPairBitsOff, &maps.bits[m], j, step * kPairOctets * K, &full[s]);
-            tc_tma_load_2d(st + kPairAlphaOff, &maps.alpha[m], (j / kGroup) * K * kOctet, step * kPairOctets, &full[s]);
-            for (int a = 0; a < p.naccs; ++a)
-              tc_tma_load_2d(st + a * kPairXBytes, &maps.act[m], step * kPairBK, t0 + a * p.n_acc, &full[s]);
-            if (++step == p.mat[m].stages) { step = 0; ++m; }
           }
+        } else {
+          const int K = p.mat[m].K;
+          const int j = rt * 256 + rank * 128;
+          if (elect_lane()) {
+            tc_arrive_expect_tx(&wfull[s], unsigned(K) * kPairOctets * (128 + 16));
+            tc_tma_load_2d(w, &maps.bits[m], j, step * kPairOctets * K, &wfull[s]);
+            tc_tma_load_2d(w + kPairBits, &maps.alpha[m], (j / kGroup) * K * kOctet, step * kPairOctets, &wfull[s]);
+          }
+          if (++step == p.mat[m].stages) { step = 0; ++m; }
         }
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
     // ---- MMA issuer: the leader's, for both CTAs ----
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      constexpr int kAStep = MODE == kGate ? 32 >> 4 : 2048 >> 4;   // 16 k further in A
+      const uint32_t base = tc_smem(smem);
+      const uint64_t a0 = MODE == kGate ? tc_desc_sw128(base + kPairAOff) : tc_desc_sw128_mn(base + kPairAOff, 8192);
+      const uint64_t x0 = tc_desc_sw128(base);
       int g = 0, i = 0;
       for (int tile = pair; tile < p.ntiles && ok; tile += npairs, ++i) {
         if (i > 0 && !pair_wait(tempty, unsigned(i - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
         for (int kb = 0; kb < p.stages; ++kb, ++g) {
           const int s = g % kPairStages;
-          if (!pair_wait(&ready[s], unsigned(g / kPairStages) & 1u)) { ok = false; break; }
+          const unsigned ph = unsigned(g / kPairStages) & 1u;
+          if (!pair_wait(&xfull[s], ph) || !pair_wait(&ready[s], ph)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t xs = tc_smem(smem + s * kPairStageBytes);
-          const uint32_t as = xs + kPairAOff;
+          const uint64_t off = uint64_t(s * (kPairStageBytes >> 4));
+          if (elect_lane()) {
 #pragma unroll
-          for (int kk = 0; kk < kPairBK / 16; ++kk) {
-            const uint64_t adesc =
-                MODE == kGate ? tc_desc_sw128(as + kk * 32) : tc_desc_sw128_mn(as + kk * 2048, 8192);
-            for (int a = 0; a < p.naccs; ++a)
-              pair_mma(tmem + uint32_t(a * 256), adesc, tc_desc_sw128(xs + a * kPairXBytes + kk * 32), p.idesc,
-                       (kb > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kPairBK / 16; ++kk) {
+              const uint64_t ad = a0 + off + uint64_t(kk * kAStep), xd = x0 + off + uint64_t(kk * (32 >> 4));
+              const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+              pair_mma(tmem, ad, xd, p.idesc, acc);
+              if (p.naccs > 1) pair_mma(tmem + 256, ad, xd + uint64_t(kPairXBytes >> 4), p.idesc, acc);
+            }
+            pair_commit(&empty[s]);
+            if (kb + 1 == p.stages) pair_commit(tfull);
           }
-          pair_commit(&empty[s]);
+          __syncwarp();
         }
-        if (!ok) break;
-        pair_commit(tfull);
       }
     }
   } else {
-    // ---- unpack warps, which also drain ----
-    const int tid = threadIdx.x - 64;
-    const bool is_up = MODE == kGate && ((tid >> 2) & 16) != 0;   // the same for a whole warp
-    uint32_t P[4] = {0u, 0u, 0u, 0u};
-    int g = 0, i = 0;
-    for (int tile = pair; tile < p.ntiles && ok; tile += npairs, ++i) {
-      int m = 0, step = 0;
-      for (int kb = 0; kb < p.stages; ++kb, ++g) {
-        const int s = g % kPairStages;
-        // the copies landing also means that the slot's previous MMAs are done
-        if (!pair_wait(&full[s], unsigned(g / kPairStages) & 1u)) { ok = false; break; }
-        unsigned char* st = smem + s * kPairStageBytes;
-        unsigned char* a = st + kPairAOff;
+    // ---- unpack warps, which also drain: group s unpacks ring slot s ----
+    const int s = (warp - kPairUnpackWarp0) / kPairGroupWarps;
+    const int gt = threadIdx.x - (kPairUnpackWarp0 + s * kPairGroupWarps) * 32;
+    unsigned char* a = smem + s * kPairStageBytes + kPairAOff;
+    const uint32_t my_ready = pair_leader(&ready[s]);
+    int g0 = 0, i = 0;   // the tile's first stage, counted over all tiles
+    for (int tile = pair; tile < p.ntiles && ok; tile += npairs, g0 += p.stages, ++i) {
+      const int first = (s - g0) & (kPairStages - 1);
+      int m = 0, step = first;
+      for (int kb = first; kb < p.stages; kb += kPairStages, step += kPairStages) {
+        const int g = g0 + kb, ws = g % kPairWStages;
+        const unsigned char* w = smem + kPairWOff + ws * kPairWBytes;
+        // the bits are there, and the slot's previous MMAs are done with its A
+        if (!pair_wait(&wfull[ws], unsigned(g / kPairWStages) & 1u) ||
+            (g >= kPairStages && !pair_wait(&empty[s], unsigned((g / kPairStages) - 1) & 1u))) {
+          ok = false;
+          break;
+        }
         if (MODE == kGate) {
-          switch (p.mat[is_up ? 1 : 0].K) {
-            case 1: unpack_gate<1>(st, a, tid, is_up, (kb & 1) == 0, P); break;
-            case 2: unpack_gate<2>(st, a, tid, is_up, (kb & 1) == 0, P); break;
-            case 3: unpack_gate<3>(st, a, tid, is_up, (kb & 1) == 0, P); break;
-            default: unpack_gate<4>(st, a, tid, is_up, (kb & 1) == 0, P); break;
+          switch (p.mat[gt >> 6].K) {   // the same for a whole warp
+            case 1: unpack_gate<1>(w, a, gt); break;
+            case 2: unpack_gate<2>(w, a, gt); break;
+            case 3: unpack_gate<3>(w, a, gt); break;
+            default: unpack_gate<4>(w, a, gt); break;
           }
         } else {
+          while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
           const int rows = p.mat[m].M - step * kPairBK;
           switch (p.mat[m].K) {
-            case 1: unpack_grad<1>(st, a, tid, rows); break;
-            case 2: unpack_grad<2>(st, a, tid, rows); break;
-            case 3: unpack_grad<3>(st, a, tid, rows); break;
-            default: unpack_grad<4>(st, a, tid, rows); break;
+            case 1: unpack_grad<1>(w, a, gt, rows); break;
+            case 2: unpack_grad<2>(w, a, gt, rows); break;
+            case 3: unpack_grad<3>(w, a, gt, rows); break;
+            default: unpack_grad<4>(w, a, gt, rows); break;
           }
-          if (++step == p.mat[m].stages) { step = 0; ++m; }
         }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // generic writes -> tensor core reads
         __syncwarp();
-        if (lane == 0) pair_arrive(pair_leader(&ready[s]));
+        if (lane == 0) {
+          pair_arrive(my_ready);
+          tc_arrive(&wempty[ws]);
+        }
       }
       if (!ok) break;
       if (!pair_wait(tfull, unsigned(i) & 1u)) { ok = false; break; }
       tc_fence_after();
-      pair_drain<MODE>(p, tmem, tile, rank, warp & 3, (warp - 2) >> 2, lane);
+      pair_drain<MODE>(p, tmem, tile, rank, warp & 3, (warp - kPairUnpackWarp0) >> 2, lane);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) pair_arrive(pair_leader(tempty));
@@ -372,7 +422,8 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   __syncthreads();
   if (s_fail != 0 && threadIdx.x == 0) {
     atomicOr(&g_pair_error, 1u);
-    tc_drain_barriers(full, 2 * kPairStages + 1);   // full, empty and tfull: copies and MMAs in flight
+    // copies and MMAs in flight: every barrier but tempty
+    tc_drain_barriers(wfull, 2 * kPairWStages + 3 * kPairStages + 1);
   }
   __syncthreads();
   __syncwarp();

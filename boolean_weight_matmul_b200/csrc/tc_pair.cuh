@@ -24,15 +24,31 @@ __device__ __forceinline__ uint32_t pair_leader(const void* p) {
   return a;
 }
 
+// Arrive on a barrier of either CTA.  What such an arrival announces is shared
+// or tensor memory of this CTA that the tensor cores will access, ordered
+// before it by fence.proxy.async or tcgen05.fence; no thread of the other CTA
+// reads this thread's writes, so the arrival needs no cluster-scope release
+// (which took 0.6 us each: it waits for all of the thread's memory operations).
 __device__ __forceinline__ void pair_arrive(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_addr) : "memory");
 }
 
-// As tc_wait, ordered after arrivals from either CTA.
+// A TMA load into this CTA's shared memory that completes on a barrier of
+// either CTA (cluster address).
+__device__ __forceinline__ void pair_tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];\n" ::"r"(tc_smem(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// As tc_wait, ordered after arrivals from either CTA.  The time is looked at
+// once in 256 tries, not on the first: reading it costs far more than a try.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, unsigned parity, unsigned long long limit = kTcWaitNs) {
   const uint32_t a = tc_smem(bar);
   unsigned long long t0 = 0;
-  for (unsigned it = 0;; ++it) {
+  for (unsigned it = 1;; ++it) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
@@ -47,6 +63,16 @@ __device__ __forceinline__ bool pair_wait(uint64_t* bar, unsigned parity, unsign
       else if (t - t0 > limit) return false;
     }
   }
+}
+
+// One lane of a converged warp.  The issuing loops below run in whole warps and
+// elect a lane only around the instructions themselves: that keeps their
+// operands in uniform registers.  Issued from inside an `if (lane == 0)` loop a
+// tcgen05.mma took 130 to 190 cycles, more than most of them run.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
 }
 
 __device__ __forceinline__ void pair_sync() {
