@@ -16,13 +16,14 @@
 //    6 stages); products of bf16 values are exact in the fp32 accumulation.
 //  * A CTA's 128 x 256 accumulator is half its tensor memory: two of them
 //    alternate, so the signed sums (8 epilogue warps: four lane quarters x two
-//    groups; three instructions per element and kernel) run while the tensor
-//    cores fill the other.
-//  * Tokens are taken in runs of at most 256, each from a zero accumulator, and
+//    groups) run while the tensor cores fill the other.
+//  * Tokens are taken in runs of at most 512, each from a zero accumulator, and
 //    the runs' signed sums are added in fp32 registers: the tensor cores' own
 //    accumulation truncates, and its error grows with the run (relative error
 //    of dalpha at 2048 tokens, 11008 x 4096: 2.6e-7 with runs of 256, 4.8e-7
 //    with 512, 1.0e-6 with 1024; fp32 products summed on the CUDA cores 4e-7).
+//    Shorter runs repeat the epilogue more often (gate and up of that size, K =
+//    3: 331 us with 256, 259 us with 512).
 //  * With few tiles the tokens are split over several pairs, whose sums land in
 //    the workspace ([split][dalpha]) and are added in order by a second kernel:
 //    deterministic.
@@ -36,7 +37,7 @@ constexpr int kDaBT = 64;                               // tokens per stage
 constexpr int kDaBlock = 64 * kDaBT * 2;                // one box: 64 tokens x 64 columns, 8 KB
 constexpr int kDaStageBytes = 4 * kDaBlock;             // two boxes of dY, two of X
 constexpr int kDaSmem = kDaStages * kDaStageBytes + 1024 + 256;
-constexpr int kDaRunStages = 4;                         // 256 tokens per run
+constexpr int kDaRunStages = 8;                         // 512 tokens per run
 constexpr int kDaEpiWarps = 8;
 constexpr int kDaThreads = (2 + kDaEpiWarps) * 32;
 constexpr unsigned kDaTmemCols = 512;
@@ -91,25 +92,37 @@ __device__ __forceinline__ DaItem da_item(const DaParams& p, int i) {
 }
 
 // S[k] += the signed sum over 32 accumulator columns: v[b] enters kernel k with
-// a plus where bit b of w[k] is set.
+// a plus where bit b of w[k] is set, taken as twice the sum over the set bits
+// minus the sum over all.  A bit test and a predicated add are two instructions
+// per element and kernel on two pipes; flipping the sign took three, two of
+// them on the logic pipe (K = 3: 281 -> 259 us at the sizes above).
 __device__ __forceinline__ void add_signed(const uint32_t v[32], const uint32_t w[MBOK_MAX_K], int K,
                                            float S[MBOK_MAX_K]) {
+  float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
+#pragma unroll
+  for (int b = 0; b < 32; b += 4) {
+    t0 += __uint_as_float(v[b]);
+    t1 += __uint_as_float(v[b + 1]);
+    t2 += __uint_as_float(v[b + 2]);
+    t3 += __uint_as_float(v[b + 3]);
+  }
+  const float total = (t0 + t1) + (t2 + t3);
 #pragma unroll
   for (int k = 0; k < MBOK_MAX_K; ++k) {
     if (k >= K) continue;
-    // opaque here: hoisted out of the runs' loop, the 32 shifted words of every
-    // kernel would not fit the registers
-    uint32_t flip = ~w[k];
-    asm volatile("" : "+r"(flip));
+    // opaque here: the tests of all kernels' bits, hoisted out of the runs'
+    // loop, would not fit the registers
+    uint32_t bits = w[k];
+    asm volatile("" : "+r"(bits));
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
     for (int b = 0; b < 32; b += 4) {
-      s0 += __uint_as_float(v[b] ^ ((flip << (31 - b)) & 0x80000000u));
-      s1 += __uint_as_float(v[b + 1] ^ ((flip << (30 - b)) & 0x80000000u));
-      s2 += __uint_as_float(v[b + 2] ^ ((flip << (29 - b)) & 0x80000000u));
-      s3 += __uint_as_float(v[b + 3] ^ ((flip << (28 - b)) & 0x80000000u));
+      if (bits & (1u << b)) s0 += __uint_as_float(v[b]);
+      if (bits & (2u << b)) s1 += __uint_as_float(v[b + 1]);
+      if (bits & (4u << b)) s2 += __uint_as_float(v[b + 2]);
+      if (bits & (8u << b)) s3 += __uint_as_float(v[b + 3]);
     }
-    S[k] += (s0 + s1) + (s2 + s3);
+    S[k] += 2.f * ((s0 + s1) + (s2 + s3)) - total;
   }
 }
 

@@ -11,10 +11,14 @@
 //
 //  * Unpacking bounds the prefill GEMM (its ALU work per weight is shared by
 //    256 tokens).  Here a pair of CTAs forms one M = 256 product of up to 512
-//    tokens: each CTA unpacks 128 rows of A per 64-deep stage, and the pair's
-//    tensor cores use every unpacked row for all 512 tokens, twice the tokens
-//    per unpacked weight at the same activation traffic (each CTA loads half of
-//    the tokens and the hardware reads both halves).
+//    tokens: each CTA unpacks 128 rows of A per 64-deep stage and loads half of
+//    the tokens, and the hardware reads both halves: a quarter of the unpacking
+//    per product.  Up to 256 tokens, two accumulators alternate and a tile is
+//    drained while the next is formed; 512 tokens take all of tensor memory, and
+//    the MMAs pause for the drain.  The wider tile is still the faster one where
+//    there are tokens for it: with 256 the unpack (about 700 cycles a stage at
+//    K = 3 against 512 for the MMAs) and its power draw bound the kernel
+//    (LLaMA-7B gate and up, 2048 tokens, input gradient: 451 us against 280).
 //  * Levels are fp16, the activations scaled to fp16 per token (scale_rows.cu):
 //    the weight's rounding is 2^-11 where bf16's is 2^-8, at the same rate.
 //    The token's inverse scale is applied to the fp32 sums.
@@ -26,43 +30,46 @@
 //    layout, so the unpack is the same and nothing is transposed.
 //
 // Per stage: TMA brings this CTA's half of the tokens, completing on the
-// leader's barrier, and the tile's bits and scales, in a ring of their own that
-// runs ahead; four unpack warps write A and arrive on the leader's `ready`
-// barrier (16 unpack warps in four groups, one per ring slot: with all 16 on
-// every stage the latency of wait, load, store, fence and arrival bounded each
-// stage at about 1 us, whatever the tokens); the leader's MMA thread issues 4 x (1 or 2) tcgen05.mma
-// (M = 256, N <= 256, K = 16) and commits the stage to both CTAs' `empty`
-// barriers.  The unpack warps also drain the accumulator (up to 512 columns,
-// all of tensor memory) after a tile's last stage: 16 warps, four per lane
-// quarter.  Every mbarrier wait is bounded (1 s): on timeout the CTA records an
-// error flag, drains what it issued (bounded) and leaves with the other.
+// leader's `ready` barrier, and the tile's bits and scales, in a ring of their
+// own that runs ahead; four unpack warps write A and arrive on the same barrier
+// (one for both: the issuing warp's waits and instructions, not the tensor
+// cores, bounded the stages with two) (16 unpack warps in four groups that take stages in turn: with all 16
+// on every stage the latency of wait, load, store, fence and arrival bounded
+// each stage at about 1 us, whatever the tokens); the leader's MMA warp issues
+// four tcgen05.mma (M = 256, N <= 256, K = 16) per accumulator and commits the
+// stage to both CTAs' `empty` barriers.  Four epilogue warps, one per
+// tensor-memory lane quarter, drain finished tiles; the unpack warps join them
+// for a CTA's last tile and for every two-accumulator tile.
+// Every mbarrier wait is bounded (1 s): on timeout the CTA records an error
+// flag, drains what it issued (bounded) and leaves with the other.
 #include "scale_rows.h"
 #include "tc_pair.cuh"
 #include "tc_unpack.cuh"
 
 namespace mbok {
 
-constexpr int kPairStages = 4;
 constexpr int kPairBK = 64;
 constexpr int kPairRows = 128;                                // A rows per CTA
-constexpr int kPairHalf = 128;                                // most tokens per CTA and accumulator
-constexpr int kPairXBytes = kPairHalf * kPairBK * 2;          // 16 KB per accumulator
 constexpr int kPairABytes = kPairRows * kPairBK * 2;          // 16 KB
 constexpr int kPairOctets = 8;                                // row octets of a bits box (64 rows)
 constexpr int kPairBits = 2 * kPairOctets * MBOK_MAX_K * 64;  // 4 KB: GATE two boxes of 64 bytes, GRAD one of 128
 constexpr int kPairAlpha = 2 * kPairOctets * MBOK_MAX_K * 16; // 1 KB
-constexpr int kPairAOff = 2 * kPairXBytes;
-constexpr int kPairStageBytes = kPairAOff + kPairABytes;      // 48 KB: tokens and A
-constexpr int kPairWStages = 6;                               // a deeper ring for the bits and scales
-constexpr int kPairWBytes = kPairBits + kPairAlpha;           // 5 KB
-constexpr int kPairWOff = kPairStages * kPairStageBytes;
-constexpr int kPairBarOff = kPairWOff + kPairWStages * kPairWBytes;
-constexpr int kPairSmem = kPairBarOff + 1024 + 256;
-constexpr int kPairUnpackWarps = 16;
-constexpr int kPairGroupWarps = kPairUnpackWarps / kPairStages;   // unpack warps per ring slot
-constexpr int kPairUnpackWarp0 = 3;                               // after the two copy warps and the MMA warp
-constexpr int kPairThreads = (kPairUnpackWarp0 + kPairUnpackWarps) * 32;
-constexpr unsigned kPairTmemCols = 512;
+constexpr int kPairWBytes = kPairBits + kPairAlpha;           // one slot of bits and scales
+// Ring slots hold A and this CTA's tokens (16 KB + 128 bytes per token): 4 for
+// tiles of 512 tokens, 6 for 256, 8 from 128 down.  Slots of bits and scales: 6
+// to 8.
+constexpr int kPairMaxSlots = 8;
+constexpr int kPairRing = 192 * 1024;
+constexpr int kPairBarriers = 512;
+constexpr int kPairSmemMax = 226 * 1024;   // of 227 KB, some of it static
+constexpr int kPairRings = kPairSmemMax - 1024 - kPairBarriers;
+constexpr int kPairGroups = 4;
+constexpr int kPairGroupWarps = 4;                            // 128 unpack threads per stage
+constexpr int kPairUnpackWarps = kPairGroups * kPairGroupWarps;
+constexpr int kPairUnpackWarp0 = 3;                           // after the two copy warps and the MMA warp
+constexpr int kPairEpiWarp0 = kPairUnpackWarp0 + kPairUnpackWarps;
+constexpr int kPairThreads = (kPairEpiWarp0 + 4) * 32;
+constexpr unsigned kPairTmemCols = 512;                       // accumulators at columns 0 and 256
 
 static __device__ unsigned int g_pair_error;
 
@@ -78,34 +85,106 @@ struct PairMaps {
   CUtensorMap act[kMaxMats];                     // GATE: one; GRAD: dY of each matrix
 };
 
+struct PairMul {
+  uint32_t pow2[8];   // 2^(15 - 2i)
+};
+
 struct PairParams {
   PairMat mat[kMaxMats];
   int nmat;
   int M, N, T;
-  int n_acc, naccs;    // tokens per accumulator (multiple of 16, <= 256), accumulators (1 or 2)
+  int n;               // tokens per tile
+  int naccs, n_acc;    // accumulators per tile (1 or 2) and tokens in each (multiple of 16, <= 256)
+  int slots, wslots;   // ring slots, and those of bits and scales
   int stages;          // per tile
   int row_tiles;       // tiles along W's rows (GATE, 128) or columns (GRAD, 256)
   int ntiles;
   uint32_t idesc;
+  PairMul mul;
   const float* inverse;   // [T rounded up to 16]
   uint16_t* out;          // H, or dX
   uint16_t* gate;         // GATE: [T][M] or nullptr
   uint16_t* up;
 };
 
+// ---- unpack ----
+//
+// As tc_unpack_row (an element is the level its K bits select), arranged for
+// the two integer pipes: the logic pipe (half rate) bounds the unpack, so
+// shifts are multiplications by powers of two on the FMA pipe where they can be
+// (factors from the kernel parameters, or the compiler would make them shifts
+// again), and one selector word serves two column pairs.
+//  * Index word: even columns' index bits (A, B) interleave into P, odd columns'
+//    into Q, and z = bytes P0 Q0 P1 Q1, so that byte 2h + e holds the 2-bit
+//    indices of the even (e = 0) or odd columns 8h .. 8h + 7.  For p < 4,
+//    ((z >> 2p) & 0x03030303) * 0x22 + 0x10101010 is the byte-permute selector of
+//    column pair p in its low half and of pair p + 4 in its high half.
+//  * Sign word: bit c of the row at bit c (c < 15) and at bit 15 + c; times
+//    2^(15 - 2i) it has the signs of columns 2i and 2i + 1 at bits 15 and 31.
+// 34 logic operations per 16 columns at K = 3 against 54.
+
+__device__ __forceinline__ uint32_t pair_index_word(uint32_t A, uint32_t B) {
+  const uint32_t P = (A & 0x5555u) | ((B + B) & 0xAAAAu);
+  const uint32_t Q = ((A >> 1) & 0x5555u) | (B & 0xAAAAu);
+  return __byte_perm(P, Q, 0x5140);
+}
+
+// lev with each half's sign flipped where the bit of kernel 0 is clear; u = the
+// sign word times 2^(15 - 2i).
+__device__ __forceinline__ uint32_t pair_sign(uint32_t u, uint32_t lev) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xA6;\n" : "=r"(r) : "r"(u), "r"(0x80008000u), "r"(lev));   // (~u & m) ^ lev
+  return r;
+}
+
+template <int K>
+__device__ __forceinline__ void pair_unpack_row(const uint32_t h[K], const uint32_t P[4], const PairMul& mul,
+                                                uint32_t out[8]) {
+  const uint32_t u0 = h[0] * 32768u + (h[0] & 0x7FFFu);
+  if (K == 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = pair_sign(u0 * mul.pow2[i], P[0]);
+    return;
+  }
+  // K = 2: the index is the two bits; K >= 3: the bits relative to kernel 0
+  const uint32_t A = K == 2 ? h[0] : ~(h[1 % K] ^ h[0]), B = K == 2 ? h[1 % K] : ~(h[2 % K] ^ h[0]);
+  const uint32_t z = pair_index_word(A, B);
+  uint32_t u3 = 0;
+  if (K == 4) {
+    const uint32_t t3 = ~(h[3 % K] ^ h[0]);
+    u3 = (t3 & 0xFFFFu) * 32768u + (t3 & 0x7FFFu);
+  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const uint32_t two = ((z >> (2 * p)) & 0x03030303u) * 0x22u + 0x10101010u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = p + 4 * e;
+      const uint32_t sel = e == 0 ? two : two >> 16;
+      uint32_t lev = __byte_perm(P[0], P[1], sel);
+      if (K == 4) {
+        const uint32_t up = __byte_perm(P[2], P[3], sel);
+        const uint32_t m = tc_prmt(u3 * mul.pow2[i], 0u, 0xBB99u);   // 16-bit masks from bits 15 and 31
+        lev = (up & m) | (lev & ~m);
+      }
+      out[i] = K == 2 ? lev : pair_sign(u0 * mul.pow2[i], lev);
+    }
+  }
+}
+
 // Four units (64 columns) of one row: the row's bits of kernel k and unit u at
 // src + k * kstride + u * 16, to the eight swizzled 16-byte chunks of `line`.
 // Units are taken in the order u ^ flip.
 template <int K>
 __device__ __forceinline__ void pair_unpack(const unsigned char* src, int kstride, const uint32_t P[4],
-                                            unsigned char* line, int r, int flip) {
+                                            const PairMul& mul, unsigned char* line, int r, int flip) {
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int u = n ^ flip;
     uint32_t h[K], out[8];
 #pragma unroll
     for (int k = 0; k < K; ++k) h[k] = *reinterpret_cast<const uint16_t*>(src + k * kstride + u * 16);
-    tc_unpack_row<K>(h, P, out);
+    pair_unpack_row<K>(h, P, mul, out);
     const int c0 = (2 * u) ^ (r & 7), c1 = (2 * u + 1) ^ (r & 7);
     *reinterpret_cast<uint4*>(line + c0 * 16) = make_uint4(out[0], out[1], out[2], out[3]);
     *reinterpret_cast<uint4*>(line + c1 * 16) = make_uint4(out[4], out[5], out[6], out[7]);
@@ -117,13 +196,13 @@ __device__ __forceinline__ void pair_unpack(const unsigned char* src, int kstrid
 // a matrix is A row 32 (m / 16) + m % 16, + 16 for up.  Eight lanes that store
 // together hold eight consecutive rows: distinct chunks.
 template <int K>
-__device__ __forceinline__ void unpack_gate(const unsigned char* w, unsigned char* a, int gt) {
+__device__ __forceinline__ void unpack_gate(const unsigned char* w, unsigned char* a, const PairMul& mul, int gt) {
   const int up = gt >> 6, m = gt & 63;
   const int o = m >> 3, i = m & 7;
   const int r = 32 * (m >> 4) + 16 * up + (m & 15);
   uint32_t P[4];
   tc_levels_f16<K>(w + kPairBits + up * (kPairAlpha / 2), o, i, false, P);
-  pair_unpack<K>(w + up * (kPairBits / 2) + o * K * 64 + 2 * i, 64, P, a + r * 128, r, 0);
+  pair_unpack<K>(w + up * (kPairBits / 2) + o * K * 64 + 2 * i, 64, P, mul, a + r * 128, r, 0);
 }
 
 // GRAD: thread gt of a group's 128 unpacks block gt & 1 (64 columns) of row
@@ -132,12 +211,14 @@ __device__ __forceinline__ void unpack_gate(const unsigned char* w, unsigned cha
 // that its chunks differ from the first's.  Rows at or beyond M are zeros:
 // their stored scales mean nothing and could be NaN.
 template <int K>
-__device__ __forceinline__ void unpack_grad(const unsigned char* w, unsigned char* a, int gt, int rows) {
+__device__ __forceinline__ void unpack_grad(const unsigned char* w, unsigned char* a, const PairMul& mul, int gt,
+                                            int rows) {
   const int r = gt >> 1, b = gt & 1;
   const int o = r >> 3, i = r & 7;
   uint32_t P[4];
   tc_levels_f16<K>(w + kPairBits, o, i, r >= rows, P);
-  pair_unpack<K>(w + o * K * 128 + b * 64 + 2 * i, 128, P, a + b * 8192 + r * 128, r, 2 * b);
+  pair_unpack<K>(w + o * K * 128 + b * 64 + 2 * i, 128, P, mul,
+                 a + b * 8192 + r * 128, r, 2 * b);
 }
 
 // 16 accumulator columns of this warp's 32 lanes.
@@ -150,59 +231,54 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t v[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
-// Store n values (n a power of two) that lanes 2i and 2i + 1 hold for rows r
-// and r + 1 at tokens t .. t + n - 1 of out [T][ld], ld even and out 4-byte
-// aligned: after one exchange per pair of tokens the even lane stores both rows
-// of the first half, the odd lane of the second, as bf16 pairs.
+// Store n values that this lane holds for row r at tokens t .. t + n - 1 of out
+// [T][ld].  With `pairs` (ld even, out 4-byte aligned) lanes 2i and 2i + 1, which
+// hold rows r and r + 1, exchange halves: the even lane stores both rows of the
+// first n / 2 tokens, the odd lane of the others, as bf16 pairs.
 template <int n>
-__device__ __forceinline__ void store_pairs(uint16_t* out, size_t ld, int rows, int T, int r, int t, const float* v,
-                                            int lane) {
-  const bool odd = lane & 1;
-  const int r0 = r & ~1;
+__device__ __forceinline__ void store_rows(bool pairs, uint16_t* out, int ld, int rows, int T, int r, int t,
+                                           const float* v, int lane) {
+  if (pairs) {
+    const bool odd = lane & 1;
+    const int r0 = r & ~1, tt = t + (odd ? n / 2 : 0);
+    const int live = r0 < rows ? T - tt : 0;   // tokens to store
+    uint16_t* at = out + size_t(tt) * ld + r0;
 #pragma unroll
-  for (int i = 0; i < n / 2; ++i) {
-    const float mine = odd ? v[i] : v[n / 2 + i];
-    const float other = __shfl_xor_sync(0xffffffffu, mine, 1);
-    const float lo = odd ? other : v[i], hi = odd ? v[n / 2 + i] : other;
-    const int tt = t + (odd ? n / 2 + i : i);
-    if (r0 < rows && tt < T) *reinterpret_cast<uint32_t*>(out + size_t(tt) * ld + r0) = tc_pack_bf16x2(lo, hi);
+    for (int i = 0; i < n / 2; ++i, at += ld) {
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[n / 2 + i], 1);
+      const uint32_t two = odd ? tc_pack_bf16x2(other, v[n / 2 + i]) : tc_pack_bf16x2(v[i], other);
+      if (i < live) *reinterpret_cast<uint32_t*>(at) = two;
+    }
+  } else {
+    const int live = r < rows ? T - t : 0;
+    uint16_t* at = out + size_t(t) * ld + r;
+#pragma unroll
+    for (int i = 0; i < n; ++i, at += ld)
+      if (i < live) *at = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
   }
 }
 
-// The same for any ld and alignment.
-template <int n>
-__device__ __forceinline__ void store_singles(uint16_t* out, size_t ld, int rows, int T, int r, int t, const float* v) {
-  if (r >= rows) return;
-#pragma unroll
-  for (int i = 0; i < n; ++i)
-    if (t + i < T) out[size_t(t + i) * ld + r] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
-}
+// silu(g) u for a bf16 result: the exponential and the quotient by the fast
+// approximations, a few 2^-22 of the value (and |g| 2^-23), far below its step.
+__device__ __forceinline__ float gated_fast(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
-template <int n>
-__device__ __forceinline__ void store_rows(bool pairs, uint16_t* out, size_t ld, int rows, int T, int r, int t,
-                                           const float* v, int lane) {
-  if (pairs) store_pairs<n>(out, ld, rows, T, r, t, v, lane);
-  else store_singles<n>(out, ld, rows, T, r, t, v);
-}
-
-// Drain this warp's share of a finished tile: lane quarter q, chunks of 16
-// tokens sub, sub + 4, ...
+// Drain one warp's share of a finished tile whose first accumulator is at
+// `tmem`: lane quarter q, chunks of 16 tokens first, first + stride, ...
 template <PairMode MODE>
-__device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, int tile, int rank, int q, int sub,
-                                           int lane) {
+__device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, int tile, int rank, int q, int lane,
+                                           int first, int stride) {
   const int per = p.n_acc / 16;
-  const int t0 = (tile / p.row_tiles) * (p.n_acc * p.naccs);
+  const int t0 = (tile / p.row_tiles) * p.n;
   const int rt = tile % p.row_tiles;
   const int rows = MODE == kGate ? p.M : p.N;
-  const size_t ld = size_t(rows);
   const bool pairs = rows % 2 == 0;   // every buffer is 16-byte aligned
   const int r = MODE == kGate ? rt * 128 + rank * 64 + 16 * q + (lane & 15) : rt * 256 + rank * 128 + 32 * q + lane;
-  for (int j = sub; j < per * p.naccs; j += kPairUnpackWarps / 4) {
-    const int a = j / per, c = j % per;
-    const int t = t0 + a * p.n_acc + 16 * c;
+  for (int j = first; j < per * p.naccs; j += stride) {
+    const int t = t0 + 16 * j;
     if (t >= p.T) break;
+    const int col = j < per ? 16 * j : 256 + 16 * (j - per);
     uint32_t w[16];
-    tmem_ld16(tmem + (uint32_t(32 * q) << 16) + uint32_t(a * 256 + 16 * c), w);
+    tmem_ld16(tmem + (uint32_t(32 * q) << 16) + uint32_t(col), w);
     float v[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -213,19 +289,19 @@ __device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, i
       v[4 * i + 3] = __uint_as_float(w[4 * i + 3]) * s.w;
     }
     if (MODE == kGrad) {
-      store_rows<16>(pairs, p.out, ld, rows, p.T, r, t, v, lane);
+      store_rows<16>(pairs, p.out, rows, rows, p.T, r, t, v, lane);
     } else {
       const bool low = lane < 16;
-      if (p.gate != nullptr) store_rows<16>(pairs, low ? p.gate : p.up, ld, rows, p.T, r, t, v, lane);
+      if (p.gate != nullptr) store_rows<16>(pairs, low ? p.gate : p.up, rows, rows, p.T, r, t, v, lane);
       // lanes l and l + 16 hold gate and up of one row: after the exchange the
       // lower lane has both for tokens t .. t + 7, the upper for t + 8 ..
       float h[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float other = __shfl_xor_sync(0xffffffffu, low ? v[8 + i] : v[i], 16);
-        h[i] = low ? gated(v[i], other) : gated(other, v[8 + i]);
+        h[i] = gated_fast(low ? v[i] : other, low ? other : v[8 + i]);
       }
-      store_rows<8>(pairs, p.out, ld, rows, p.T, r, low ? t : t + 8, h, lane);
+      store_rows<8>(pairs, p.out, rows, rows, p.T, r, low ? t : t + 8, h, lane);
     }
   }
 }
@@ -236,32 +312,36 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(smem + kPairBarOff);   // bits and scales landed
-  uint64_t* wempty = wfull + kPairWStages; // ... and unpacked
-  uint64_t* xfull = wempty + kPairWStages; // leader: both CTAs' tokens landed
-  uint64_t* ready = xfull + kPairStages;   // leader: both CTAs' A is unpacked
-  uint64_t* empty = ready + kPairStages;   // the stage's MMAs are done (both CTAs)
-  uint64_t* tfull = empty + kPairStages;   // the accumulator holds a finished tile (both CTAs)
-  uint64_t* tempty = tfull + 1;            // leader: both CTAs drained the accumulator
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 1);
+  const int x_bytes = p.n_acc / 2 * 128;                    // this CTA's tokens of one accumulator
+  const int slot_bytes = kPairABytes + p.naccs * x_bytes;   // A, then tokens
+  unsigned char* wring = smem + p.slots * slot_bytes;
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(wring + p.wslots * kPairWBytes);   // bits and scales landed
+  uint64_t* wempty = wfull + kPairMaxSlots;   // ... and unpacked
+  uint64_t* ready = wempty + kPairMaxSlots;   // leader: both CTAs' tokens landed and their A is unpacked
+  uint64_t* empty = ready + kPairMaxSlots;    // the stage's MMAs are done (both CTAs)
+  uint64_t* tfull = empty + kPairMaxSlots;    // accumulator b holds a finished tile (both CTAs)
+  uint64_t* last_full = tfull + 2;            // the CTA's last tile is finished (completes once; both CTAs)
+  uint64_t* tempty = last_full + 1;           // leader: both CTAs drained accumulator b
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   __shared__ int s_fail;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(pair_rank());
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int n_mine = (p.ntiles - 1 - pair) / npairs + 1;   // tiles pair, pair + npairs, ...; at least one
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairWStages; ++s) {
+    for (int s = 0; s < kPairMaxSlots; ++s) {
       tc_mbar_init(&wfull[s], 1);
       tc_mbar_init(&wempty[s], kPairGroupWarps);
-    }
-    for (int s = 0; s < kPairStages; ++s) {
-      tc_mbar_init(&xfull[s], 1);
-      tc_mbar_init(&ready[s], 2 * kPairGroupWarps);
+      tc_mbar_init(&ready[s], 2 * kPairGroupWarps + 1);   // + the leader's expectation of the tokens
       tc_mbar_init(&empty[s], 1);
     }
-    tc_mbar_init(tfull, 1);
-    tc_mbar_init(tempty, 2 * kPairUnpackWarps);
+    for (int b = 0; b < 2; ++b) {
+      tc_mbar_init(&tfull[b], 1);
+      tc_mbar_init(&tempty[b], 2 * (p.naccs > 1 ? 4 + kPairUnpackWarps : 4));
+    }
+    tc_mbar_init(last_full, 1);
     s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
@@ -274,40 +354,42 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
 
+  // Every role walks the stages of all its tiles with a slot index and the
+  // parity of the slot's current use.
   if (warp == 0) {
     // ---- token copies ----
-    const int n_half = p.n_acc / 2;
-    const unsigned bytes = unsigned(2 * p.naccs * n_half * kPairBK * 2);   // both CTAs'
-    int g = 0;
+    const unsigned bytes = unsigned(p.n * kPairBK * 2);   // both CTAs'
+    int s = 0, g = 0;
+    unsigned ph = 1;   // parity of the slot's previous use
     for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
-      const int t0 = (tile / p.row_tiles) * (p.n_acc * p.naccs) + rank * n_half;
+      const int t0 = (tile / p.row_tiles) * p.n + rank * (p.n_acc / 2);
       int m = 0, step = 0;   // GRAD: matrix and its 64-row step
       for (int kb = 0; kb < p.stages; ++kb, ++g) {
-        const int s = g % kPairStages;
-        if (g >= kPairStages && !pair_wait(&empty[s], unsigned((g / kPairStages) - 1) & 1u)) { ok = false; break; }
-        unsigned char* st = smem + s * kPairStageBytes;
-        const uint32_t bar = pair_leader(&xfull[s]);
+        if (g >= p.slots && !pair_wait(&empty[s], ph)) { ok = false; break; }
+        const uint32_t bar = pair_leader(&ready[s]);
         const CUtensorMap* map = &maps.act[MODE == kGate ? 0 : m];
-        const int x = (MODE == kGate ? kb : step) * kPairBK;
         if (elect_lane()) {
-          if (rank == 0) tc_arrive_expect_tx(&xfull[s], bytes);
-          pair_tma_load_2d(st, map, x, t0, bar);
-          if (p.naccs > 1) pair_tma_load_2d(st + kPairXBytes, map, x, t0 + p.n_acc, bar);
+          if (rank == 0) tc_arrive_expect_tx(&ready[s], bytes);
+          unsigned char* x = smem + s * slot_bytes + kPairABytes;
+          const int k0 = (MODE == kGate ? kb : step) * kPairBK;
+          pair_tma_load_2d(x, map, k0, t0, bar);
+          if (p.naccs > 1) pair_tma_load_2d(x + x_bytes, map, k0, t0 + p.n_acc, bar);
         }
         __syncwarp();
         if (MODE == kGrad && ++step == p.mat[m].stages) { step = 0; ++m; }
+        if (++s == p.slots) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 2) {
     // ---- copies of bits and scales ----
-    int g = 0;
+    int s = 0, g = 0;
+    unsigned ph = 1;
     for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
       const int rt = tile % p.row_tiles;
       int m = 0, step = 0;
       for (int kb = 0; kb < p.stages; ++kb, ++g) {
-        const int s = g % kPairWStages;
-        if (g >= kPairWStages && !pair_wait(&wempty[s], unsigned((g / kPairWStages) - 1) & 1u)) { ok = false; break; }
-        unsigned char* w = smem + kPairWOff + s * kPairWBytes;
+        if (g >= p.wslots && !pair_wait(&wempty[s], ph)) { ok = false; break; }
+        unsigned char* w = wring + s * kPairWBytes;
         if (MODE == kGate) {
           const int o = (rt * 128 + rank * 64) / kOctet;
           if (elect_lane()) {
@@ -330,6 +412,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
           if (++step == p.mat[m].stages) { step = 0; ++m; }
         }
         __syncwarp();
+        if (++s == p.wslots) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 1) {
@@ -337,83 +420,109 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     if (rank == 0) {
       constexpr int kAStep = MODE == kGate ? 32 >> 4 : 2048 >> 4;   // 16 k further in A
       const uint32_t base = tc_smem(smem);
-      const uint64_t a0 = MODE == kGate ? tc_desc_sw128(base + kPairAOff) : tc_desc_sw128_mn(base + kPairAOff, 8192);
-      const uint64_t x0 = tc_desc_sw128(base);
-      int g = 0, i = 0;
-      for (int tile = pair; tile < p.ntiles && ok; tile += npairs, ++i) {
-        if (i > 0 && !pair_wait(tempty, unsigned(i - 1) & 1u)) { ok = false; break; }
+      const uint64_t a0 = MODE == kGate ? tc_desc_sw128(base) : tc_desc_sw128_mn(base, 8192);
+      const uint64_t x0 = tc_desc_sw128(base + kPairABytes);
+      int s = 0;
+      unsigned ph = 0;
+      for (int i = 0; i < n_mine && ok; ++i) {
+        // one accumulator per tile: tiles alternate between two; else all tiles use both
+        const int b = p.naccs > 1 ? 0 : i & 1, use = p.naccs > 1 ? i : i >> 1;
+        if (use > 0 && !pair_wait(&tempty[b], unsigned(use - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
-        for (int kb = 0; kb < p.stages; ++kb, ++g) {
-          const int s = g % kPairStages;
-          const unsigned ph = unsigned(g / kPairStages) & 1u;
-          if (!pair_wait(&xfull[s], ph) || !pair_wait(&ready[s], ph)) { ok = false; break; }
+        const uint32_t d = tmem + uint32_t(b * 256);
+        for (int kb = 0; kb < p.stages; ++kb) {
+          if (!pair_wait(&ready[s], ph)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t off = uint64_t(s * (kPairStageBytes >> 4));
+          const uint64_t off = uint64_t((s * slot_bytes) >> 4);
           if (elect_lane()) {
 #pragma unroll
             for (int kk = 0; kk < kPairBK / 16; ++kk) {
               const uint64_t ad = a0 + off + uint64_t(kk * kAStep), xd = x0 + off + uint64_t(kk * (32 >> 4));
               const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
-              pair_mma(tmem, ad, xd, p.idesc, acc);
-              if (p.naccs > 1) pair_mma(tmem + 256, ad, xd + uint64_t(kPairXBytes >> 4), p.idesc, acc);
+              pair_mma(d, ad, xd, p.idesc, acc);
+              if (p.naccs > 1) pair_mma(d + 256, ad, xd + uint64_t(x_bytes >> 4), p.idesc, acc);
             }
             pair_commit(&empty[s]);
-            if (kb + 1 == p.stages) pair_commit(tfull);
+            if (kb + 1 == p.stages) {
+              pair_commit(&tfull[b]);
+              if (i + 1 == n_mine) pair_commit(last_full);
+            }
           }
           __syncwarp();
+          if (++s == p.slots) { s = 0; ph ^= 1u; }
         }
       }
     }
-  } else {
-    // ---- unpack warps, which also drain: group s unpacks ring slot s ----
-    const int s = (warp - kPairUnpackWarp0) / kPairGroupWarps;
-    const int gt = threadIdx.x - (kPairUnpackWarp0 + s * kPairGroupWarps) * 32;
-    unsigned char* a = smem + s * kPairStageBytes + kPairAOff;
-    const uint32_t my_ready = pair_leader(&ready[s]);
-    int g0 = 0, i = 0;   // the tile's first stage, counted over all tiles
-    for (int tile = pair; tile < p.ntiles && ok; tile += npairs, g0 += p.stages, ++i) {
-      const int first = (s - g0) & (kPairStages - 1);
+  } else if (warp < kPairEpiWarp0) {
+    // ---- unpack warps: group `grp` takes every fourth stage ----
+    const int grp = (warp - kPairUnpackWarp0) / kPairGroupWarps;
+    const int gt = threadIdx.x - (kPairUnpackWarp0 + grp * kPairGroupWarps) * 32;
+    int s = grp, ws = grp, g = grp, first = grp;   // both rings have at least kPairGroups slots
+    unsigned ph = 0, wph = 0;
+    for (int i = 0; i < n_mine && ok; ++i) {
       int m = 0, step = first;
-      for (int kb = first; kb < p.stages; kb += kPairStages, step += kPairStages) {
-        const int g = g0 + kb, ws = g % kPairWStages;
-        const unsigned char* w = smem + kPairWOff + ws * kPairWBytes;
+      int kb = first;
+      for (; kb < p.stages; kb += kPairGroups, step += kPairGroups, g += kPairGroups) {
+        const unsigned char* w = wring + ws * kPairWBytes;
+        unsigned char* a = smem + s * slot_bytes;
         // the bits are there, and the slot's previous MMAs are done with its A
-        if (!pair_wait(&wfull[ws], unsigned(g / kPairWStages) & 1u) ||
-            (g >= kPairStages && !pair_wait(&empty[s], unsigned((g / kPairStages) - 1) & 1u))) {
-          ok = false;
-          break;
-        }
+        if (!pair_wait(&wfull[ws], wph) || (g >= p.slots && !pair_wait(&empty[s], ph ^ 1u))) { ok = false; break; }
         if (MODE == kGate) {
           switch (p.mat[gt >> 6].K) {   // the same for a whole warp
-            case 1: unpack_gate<1>(w, a, gt); break;
-            case 2: unpack_gate<2>(w, a, gt); break;
-            case 3: unpack_gate<3>(w, a, gt); break;
-            default: unpack_gate<4>(w, a, gt); break;
+            case 1: unpack_gate<1>(w, a, p.mul, gt); break;
+            case 2: unpack_gate<2>(w, a, p.mul, gt); break;
+            case 3: unpack_gate<3>(w, a, p.mul, gt); break;
+            default: unpack_gate<4>(w, a, p.mul, gt); break;
           }
         } else {
           while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
           const int rows = p.mat[m].M - step * kPairBK;
           switch (p.mat[m].K) {
-            case 1: unpack_grad<1>(w, a, gt, rows); break;
-            case 2: unpack_grad<2>(w, a, gt, rows); break;
-            case 3: unpack_grad<3>(w, a, gt, rows); break;
-            default: unpack_grad<4>(w, a, gt, rows); break;
+            case 1: unpack_grad<1>(w, a, p.mul, gt, rows); break;
+            case 2: unpack_grad<2>(w, a, p.mul, gt, rows); break;
+            case 3: unpack_grad<3>(w, a, p.mul, gt, rows); break;
+            default: unpack_grad<4>(w, a, p.mul, gt, rows); break;
           }
         }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // generic writes -> tensor core reads
         __syncwarp();
         if (lane == 0) {
-          pair_arrive(my_ready);
+          pair_arrive(pair_leader(&ready[s]));
           tc_arrive(&wempty[ws]);
         }
+        if ((s += kPairGroups) >= p.slots) { s -= p.slots; ph ^= 1u; }
+        if ((ws += kPairGroups) >= p.wslots) { ws -= p.wslots; wph ^= 1u; }
       }
+      first = kb - p.stages;   // this group's first stage of the next tile
       if (!ok) break;
-      if (!pair_wait(tfull, unsigned(i) & 1u)) { ok = false; break; }
+      // Two accumulators: every tile is drained by all warps.  One: only the
+      // last tile, on a barrier that completes once (a parity wait on tfull from
+      // here could pass on an earlier phase, since these warps do not wait for
+      // every tile).
+      const bool last = i + 1 == n_mine;
+      if (p.naccs > 1 || last) {
+        if (!(p.naccs > 1 ? pair_wait(&tfull[0], unsigned(i) & 1u) : pair_wait(last_full, 0u))) { ok = false; break; }
+        tc_fence_after();
+        const int b = p.naccs > 1 ? 0 : i & 1;
+        pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair + i * npairs, rank, warp & 3, lane,
+                         1 + (warp - kPairUnpackWarp0) / 4, 1 + kPairUnpackWarps / 4);
+        tc_fence_before();
+        __syncwarp();
+        if (p.naccs > 1 && lane == 0) pair_arrive(pair_leader(&tempty[0]));
+      }
+    }
+  } else {
+    // ---- epilogue: lane quarter warp & 3 ----
+    for (int i = 0; i < n_mine; ++i) {
+      const int b = p.naccs > 1 ? 0 : i & 1, use = p.naccs > 1 ? i : i >> 1;
+      if (!pair_wait(&tfull[b], unsigned(use) & 1u)) { ok = false; break; }
       tc_fence_after();
-      pair_drain<MODE>(p, tmem, tile, rank, warp & 3, (warp - kPairUnpackWarp0) >> 2, lane);
+      const bool shared = p.naccs > 1 || i + 1 == n_mine;   // with the unpack warps: every fifth chunk
+      pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair + i * npairs, rank, warp & 3, lane, 0,
+                       shared ? 1 + kPairUnpackWarps / 4 : 1);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) pair_arrive(pair_leader(tempty));
+      if (lane == 0) pair_arrive(pair_leader(&tempty[b]));
     }
   }
 
@@ -423,7 +532,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   if (s_fail != 0 && threadIdx.x == 0) {
     atomicOr(&g_pair_error, 1u);
     // copies and MMAs in flight: every barrier but tempty
-    tc_drain_barriers(wfull, 2 * kPairWStages + 3 * kPairStages + 1);
+    tc_drain_barriers(wfull, 4 * kPairMaxSlots + 3);
   }
   __syncthreads();
   __syncwarp();
@@ -451,13 +560,13 @@ template <PairMode MODE>
 static int pair_count() {
   const void* fn = reinterpret_cast<const void*>(gemm_pair_kernel<MODE>);
   static PerDeviceOnce attr_once;
-  if (set_smem_attr_once(attr_once, fn, kPairSmem) != cudaSuccess) return 0;
+  if (set_smem_attr_once(attr_once, fn, kPairSmemMax) != cudaSuccess) return 0;
   static PerDeviceValue<int> cache;
   return cache.get(current_device(), [fn]() -> int {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.dynamicSmemBytes = kPairSmemMax;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -471,16 +580,17 @@ static int pair_count() {
 }
 
 // Tokens per tile (a multiple of 32, at most 512) that minimises the time of
-// the wave-quantised grid; a tile costs its tokens, and at least what unpacking
-// its weights costs (about 256 tokens' worth of tensor-core time).
-static int pair_token_tile(int row_tiles, int T, int pairs) {
+// the wave-quantised grid.  A stage costs its tokens' MMAs, and at least the
+// unpack of its weights (about 320 tokens' worth); a tile of more than 256
+// tokens adds its drain, about 10 stages' worth.
+static int pair_token_tile(int row_tiles, int stages, int T, int pairs) {
   if (pairs < 1) pairs = 1;
   int best = 512;
-  long best_cost = -1;
+  double best_cost = -1;
   const int most = T >= 512 ? 512 : (T + 31) / 32 * 32;
   for (int n = most; n >= 32; n -= 32) {
     const long tiles = long(row_tiles) * ((T + n - 1) / n);
-    const long cost = (tiles + pairs - 1) / pairs * (n > 256 ? n : 256);
+    const double cost = double((tiles + pairs - 1) / pairs) * (n > 320 ? n : 320) * (stages + (n > 256 ? 10 : 0));
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = n;
@@ -493,12 +603,19 @@ template <PairMode MODE>
 static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t stream) {
   const int pairs = pair_count<MODE>();
   if (pairs < 1) return cudaErrorNotSupported;
+  const int slot_bytes = kPairABytes + p.n / 2 * 128;
+  p.slots = kPairRing / slot_bytes < kPairMaxSlots ? kPairRing / slot_bytes : kPairMaxSlots;
+  const int wslots = (kPairRings - p.slots * slot_bytes) / kPairWBytes;
+  p.wslots = wslots < kPairMaxSlots ? wslots : kPairMaxSlots;
+  for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
+  const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
   const int grid = 2 * (p.ntiles < pairs ? p.ntiles : pairs);
-  gemm_pair_kernel<MODE><<<grid, kPairThreads, kPairSmem, stream>>>(maps, p);
+  gemm_pair_kernel<MODE><<<grid, kPairThreads, smem, stream>>>(maps, p);
   return cudaGetLastError();
 }
 
 static void set_tokens(PairParams& p, int n) {
+  p.n = n;
   p.naccs = n > 256 ? 2 : 1;
   p.n_acc = n / p.naccs;   // n is a multiple of 32
   p.ntiles = p.row_tiles * ((p.T + n - 1) / n);
@@ -526,7 +643,7 @@ cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_
   p.T = T;
   p.stages = gate.N / kPairBK;
   p.row_tiles = (gate.M + 127) / 128;
-  set_tokens(p, pair_token_tile(p.row_tiles, T, pair_count<kGate>()));
+  set_tokens(p, pair_token_tile(p.row_tiles, p.stages, T, pair_count<kGate>()));
   p.idesc = tc_idesc_f16(256, p.n_acc, false, false, false);
   p.inverse = inverse;
   p.out = H;
@@ -573,7 +690,11 @@ cudaError_t launch_gemm_grad_x(int nmat, const uint8_t* const* packed, const uin
   p.N = shapes[0].N;
   p.T = T;
   p.row_tiles = (p.N + 255) / 256;
-  set_tokens(p, pair_token_tile(p.row_tiles, T, pair_count<kGrad>()));
+  for (int i = 0; i < nmat; ++i) {
+    p.mat[i].stages = (shapes[i].M + kPairBK - 1) / kPairBK;
+    p.stages += p.mat[i].stages;
+  }
+  set_tokens(p, pair_token_tile(p.row_tiles, p.stages, T, pair_count<kGrad>()));
   p.idesc = tc_idesc_f16(256, p.n_acc, false, true, false);
   p.inverse = inverse;
   p.out = dX;
@@ -582,8 +703,6 @@ cudaError_t launch_gemm_grad_x(int nmat, const uint8_t* const* packed, const uin
     const Shape& s = shapes[i];
     p.mat[i].K = s.K;
     p.mat[i].M = s.M;
-    p.mat[i].stages = (s.M + kPairBK - 1) / kPairBK;
-    p.stages += p.mat[i].stages;
     good = good &&
            make_map(&maps.act[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dys[i], ld[i], T, uint64_t(ld[i]) * 2, kPairBK,
                     p.n_acc / 2, true) &&
