@@ -51,6 +51,7 @@ cudaError_t launch_gemm_backward(int, const uint8_t* const*, const uint16_t* con
                                  int, const uint16_t* const*, uint16_t*, float* const*, void*, cudaStream_t);
 unsigned gemm_pair_error_flags();
 unsigned gemm_dalpha_error_flags();
+unsigned distill_error_flags();
 cudaError_t launch_distill_loss(const void*, bool, int, int, size_t, const float*, const int*, int, float,
                                 const float*, float*, float*, void*, size_t, cudaStream_t);
 cudaError_t launch_distill_backward(const void*, bool, int, int, size_t, const float*, const int*, int, float,
@@ -520,8 +521,9 @@ int mbok_read_device_errors(unsigned* flags) {
   const unsigned d = gemv_gated_error_flags();
   const unsigned p = gemm_pair_error_flags();
   const unsigned a = gemm_dalpha_error_flags();
-  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u || p == ~0u || a == ~0u) return MBOK_ERR_CUDA;
-  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u) | ((p | a) ? 8u : 0u);
+  const unsigned l = distill_error_flags();
+  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u || p == ~0u || a == ~0u || l == ~0u) return MBOK_ERR_CUDA;
+  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u) | ((p | a) ? 8u : 0u) | (l ? 16u : 0u);
   return MBOK_OK;
 }
 

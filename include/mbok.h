@@ -365,8 +365,9 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
  * An entry whose index lies outside [0, V) (say -1, padding a short list) or
  * whose teacher logit is -infinity is not listed; an index given twice counts
  * twice.  A token of weight 0, or with nothing listed, has loss 0, lse 0 and
- * gradient 0 whatever its logits.  Logits of -infinity have probability 0; a
- * row with no other, or with +infinity or NaN, gives NaN.
+ * gradient 0 whatever its logits.  Logits of -infinity (or the type's lowest
+ * value) have probability 0; a row with no other, with +infinity or NaN, or
+ * whose largest logit times log2(e) / tau overflows fp32, gives NaN.
  *   logits  : fp32 (dtype MBOK_F32) or bf16 (MBOK_BF16) [T][V], rows `ld`
  *             elements apart (ld >= V), 16-byte aligned (the first row).
  *   teacher : fp32 [T][top].   index: int32 [T][top].   1 <= top <= MBOK_DISTILL_MAX_TOP.
@@ -375,8 +376,7 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
  *   loss, lse : out, fp32 [T].
  *   dlogits : out, as logits with rows ld_dlogits apart, or NULL for the loss
  *             alone; may be `logits` itself (then with the same ld).
- * With dlogits each logit is read once for rows of up to 262144 bf16 or
- * 131072 fp32 values.  Sums are fp32 in a fixed order: deterministic.
+ * Sums are fp32 in a fixed order: deterministic.
  * 1 <= T <= 2^23, 1 <= V <= MBOK_DISTILL_MAX_VOCAB. */
 int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
                       const int32_t* index, int top, float temperature, const float* weight, float* loss, float* lse,
@@ -462,7 +462,8 @@ int mbok_gemv_noalloc(const uint32_t* packed, const uint16_t* alpha, int K, int 
  * *flags (0 = none; bit 0 = a whole-row lookup GEMV copy wait gave up, in
  * which case that CTA stored none of its rows of y; bit 1 = a prefill-GEMM
  * pipeline wait gave up; bit 2 = a tensor-core GEMV copy wait gave up, bit 3 = a
- * CTA-pair GEMM (mbok_gemm_gated, mbok_gemm_backward) pipeline wait gave up, in
+ * CTA-pair GEMM (mbok_gemm_gated, mbok_gemm_backward) pipeline wait gave up,
+ * bit 4 = a copy wait of mbok_distill_loss gave up, in
  * which case that launch stored no outputs) and clears them.  Synchronises
  * the device.  Returns MBOK_ERR_CUDA if the flags cannot be read. */
 int mbok_read_device_errors(unsigned* flags);

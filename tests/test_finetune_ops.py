@@ -701,3 +701,37 @@ def test_gemm_calls_captured_and_on_another_stream():
     for _ in range(2):
         graph.replay()
         check()
+
+
+@pytest.mark.parametrize("dtype,V,T", [("bf16", 2053, 1300), ("f32", 1000, 700), ("bf16", 8, 610), ("f32", 3, 600)])
+def test_distill_many_rows(dtype, V, T):
+    # more rows than SMs keep in flight, rows of every alignment, masked rows among them; fused, in place and apart
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    top, tau = min(V, 24), 2.0
+    z, teacher, index, weight, grad = _distill_case(T, V, top, 21, dtype)
+    weight[::7] = 0.0
+    # rows far from zero on either side, and rows where most logits are masked
+    z[4::9] += 300.0
+    z[5::9] -= 300.0
+    listed = torch.zeros(T, V, dtype=torch.bool)
+    rows = torch.arange(T)[:, None].expand(T, top)
+    ok = torch.from_numpy((index >= 0) & (index < V))
+    listed[rows[ok], torch.from_numpy(index)[ok].long()] = True
+    z[6::9] = torch.where(listed[6::9], z[6::9], torch.full_like(z[6::9], float("-inf")))
+    td, xd, wd = to_dev(teacher), to_dev(index), to_dev(weight)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    ones = np.ones_like(grad)
+    for ld_dz in (V, V + 1):
+        buf = torch.full((T, ld_dz), 7.0, dtype=_dt(dtype), device="cuda")
+        mb.distill_loss(z.cuda(), _code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse, buf, ld_dz)
+        torch.cuda.synchronize()
+        assert mb.read_device_errors() == 0
+        _check_distill(z, teacher, index, weight, ones, tau, V, dtype, _f64(loss), _f64(lse), _f64(buf[:, :V]))
+        assert (buf[:, V:] == 7.0).all()
+        if ld_dz == V:
+            first = buf.clone()
+    zd = z.cuda()
+    mb.distill_loss(zd, _code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse, zd, V)
+    torch.cuda.synchronize()
+    assert torch.equal(zd, first)
