@@ -36,10 +36,9 @@ cudaError_t launch_gemv_lut_multi(int, const uint8_t* const*, const uint16_t* co
                                   const void*, bool, float*, void*, cudaStream_t, bool);
 size_t gemv_multi_workspace_bytes(int, const int*, const int*, int);
 
-size_t gemv_gated_workspace_bytes(const Shape&);
+size_t gemv_gated_workspace_bytes(const Shape&, int);
 cudaError_t launch_gemv_gated(const uint8_t*, const uint16_t*, const Shape&, const uint8_t*, const uint16_t*,
                               const Shape&, const void*, bool, int, void*, bool, void*, cudaStream_t, bool);
-unsigned gemv_gated_error_flags();
 cudaError_t launch_gated_backward(const uint16_t*, const uint16_t*, const uint16_t*, size_t, uint16_t*, uint16_t*,
                                   uint16_t*, cudaStream_t);
 size_t gemm_gated_workspace_bytes(int, int);
@@ -319,8 +318,8 @@ int mbok_gemv_multi(int nseg, const uint32_t* const* packed, const uint16_t* con
 
 size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int batch) {
   if (check_shape(K_gate, M, N) != MBOK_OK || check_shape(K_up, M, N) != MBOK_OK) return 0;
-  if (batch != 1) return 0;   // the tensor-core kernel needs none (nor does a bad batch)
-  return gemv_gated_workspace_bytes(make_shape(K_gate, M, N));
+  if (batch < 1 || batch > MBOK_MAX_BATCH) return 0;
+  return gemv_gated_workspace_bytes(make_shape(K_gate, M, N), batch);
 }
 
 int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
@@ -339,7 +338,7 @@ int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int
       !aligned(x, 16) || !aligned(h, dtype_bytes(h_dtype)))
     return MBOK_ERR_ALIGN;
   const Shape gate = make_shape(K_gate, M, N), up = make_shape(K_up, M, N);
-  const size_t need = batch == 1 ? gemv_gated_workspace_bytes(gate) : 0;
+  const size_t need = gemv_gated_workspace_bytes(gate, batch);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
     return MBOK_ERR_WORKSPACE;
   return from_cuda(launch_gemv_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate, gate,
@@ -518,12 +517,11 @@ int mbok_read_device_errors(unsigned* flags) {
   const unsigned g = gemv_lut4_error_flags();
   const unsigned m = gemm_error_flags();
   const unsigned t = gemv_mma_error_flags();
-  const unsigned d = gemv_gated_error_flags();
   const unsigned p = gemm_pair_error_flags();
   const unsigned a = gemm_dalpha_error_flags();
   const unsigned l = distill_error_flags();
-  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u || p == ~0u || a == ~0u || l == ~0u) return MBOK_ERR_CUDA;
-  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u) | ((p | a) ? 8u : 0u) | (l ? 16u : 0u);
+  if (g == ~0u || m == ~0u || t == ~0u || p == ~0u || a == ~0u || l == ~0u) return MBOK_ERR_CUDA;
+  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | (t ? 4u : 0u) | ((p | a) ? 8u : 0u) | (l ? 16u : 0u);
   return MBOK_OK;
 }
 

@@ -671,7 +671,7 @@ size_t gemv_multi_workspace_bytes(int nseg, const int* K, const int* M, int N) {
 
 // Partial sums of the gated form: both matrices' regions, also with one slab
 // (the projections meet only in the combine).
-size_t gemv_gated_workspace_bytes(const Shape& s) {
+size_t gemv_gated_lut_workspace_bytes(const Shape& s) {
   const size_t nslab = size_t((s.N + kSlabCols - 1) / kSlabCols);
   return 2 * nslab * size_t(s.O) * kOctet * sizeof(float);
 }
@@ -794,7 +794,7 @@ cudaError_t launch_gemv_lut_multi(int nseg, const uint8_t* const* packed, const 
 }
 
 // h = silu(W_gate x) * (W_up x) for one vector; workspace as sized by
-// gemv_gated_workspace_bytes.  With one slab the main launch's outputs (not
+// gemv_gated_lut_workspace_bytes.  With one slab the main launch's outputs (not
 // partials) go to the workspace, which the combine reads the same way.
 cudaError_t launch_gemv_lut_gated(const uint8_t* packed_gate, const uint16_t* alpha_gate, const Shape& gate,
                                   const uint8_t* packed_up, const uint16_t* alpha_up, const Shape& up, const void* x,

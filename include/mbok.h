@@ -270,8 +270,8 @@ int mbok_gemv_multi(int nseg, const uint32_t* const* packed, const uint16_t* con
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace mbok_gemv_gated needs (same rules as
- * mbok_gemv_workspace_bytes): both projections' partial sums for one vector,
- * 0 for more.  0 on a bad argument. */
+ * mbok_gemv_workspace_bytes): both projections' partial sums of column slabs,
+ * always for one vector, for wide N for more.  0 on a bad argument. */
 size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int batch);
 
 /* The gated feed-forward block's first half for a decode step: two
@@ -286,7 +286,8 @@ size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int b
  *   mbok_gemv_gated_workspace_bytes; mbok_gemv_set_static_weights applies).
  * One vector runs on the lookup kernel (one launch over both matrices and the
  * small launch that adds the slabs' partials and gates), two to 16 on the
- * tensor-core kernel (one launch per 16 bf16 or 5 fp32 vectors).
+ * tensor cores (one launch per 16 bf16 or 5 fp32 vectors, and for wide N a
+ * small one that adds column slabs).
  * g and u have the accuracy of mbok_gemv; deterministic. */
 int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
                     const uint16_t* alpha_up, int K_up, int M, int N, int group, const void* x, int x_dtype, int batch,

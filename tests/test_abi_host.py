@@ -236,7 +236,9 @@ def test_gemv_gated_sizes_and_argument_errors(L):
     # both projections' partials [N/512 slabs][O * 8], with one slab too; none for more than one vector
     assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 1) == 2 * 8 * O(100) * 8 * 4
     assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 128, 1) == 2 * O(100) * 8 * 4
-    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 2) == 0
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 2) == 0      # one CTA covers 4096 columns
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 11008, 2) >= 3 * 2 * 2 * 100 * 4
+    assert L.mbok_gemv_gated_workspace_bytes(3, 2, 100, 4096, 17) == 0
     assert L.mbok_gemv_gated_workspace_bytes(0, 2, 100, 4096, 1) == 0
     g = lambda **kw: L.mbok_gemv_gated(*[kw.get(k, v) for k, v in dict(
         pg=FAKE, ag=FAKE, Kg=3, pu=FAKE, au=FAKE, Ku=2, M=64, N=1024, group=128, x=FAKE, dt=1, batch=1, h=FAKE, hd=1,

@@ -103,8 +103,8 @@ def _gemv_gated(gate, up, xd, x_dtype, batch, out):
 
 
 @pytest.mark.parametrize("kg,ku", [(1, 1), (3, 3), (4, 1), (2, 4)])
-@pytest.mark.parametrize("M,N", [(1, 128), (7, 512), (13, 640), (129, 1024), (200, 4224)])
-@pytest.mark.parametrize("batch", [1, 2, 5, 16])
+@pytest.mark.parametrize("M,N", [(1, 128), (7, 512), (13, 640), (129, 1024), (200, 4224), (40, 5248)])
+@pytest.mark.parametrize("batch", [1, 2, 5, 8, 16])
 def test_gemv_gated(kg, ku, M, N, batch):
     gate, up = Layer(kg, M, N, 9000 + kg + M, pad_nan=True), Layer(ku, M, N, 9100 + ku + N, pad_nan=True)
     for x_dtype, out in (("bf16", "bf16"), ("f32", "f32")):
@@ -114,6 +114,18 @@ def test_gemv_gated(kg, ku, M, N, batch):
         u, Eu = F.project(up.words, up.alpha, ku, M, N, x64)
         want = F.silu(g) * u
         _assert_within(_f64(h), want, _gated_tol(g, Eg, u, Eu, N * max(kg, ku), want, out), f"{x_dtype} -> {out}")
+
+
+def test_gemv_gated_many_rows():
+    # several octets per warp: the ring wraps, the sums' two buffers alternate
+    for M, N, batch in ((5000, 256, 3), (2600, 4096, 9), (1300, 5376, 2)):
+        gate, up = Layer(3, M, N, 31), Layer(2, M, N, 32)
+        x, x64 = _x(batch, N, 33, "bf16")
+        h = _gemv_gated(gate, up, x_dev(x, "bf16"), "bf16", batch, "f32")
+        g, Eg = F.project(gate.words, gate.alpha, 3, M, N, x64)
+        u, Eu = F.project(up.words, up.alpha, 2, M, N, x64)
+        want = F.silu(g) * u
+        _assert_within(_f64(h), want, _gated_tol(g, Eg, u, Eu, N * 3, want, "f32"))
 
 
 def test_gemv_gated_mixed_types_and_alignment():
