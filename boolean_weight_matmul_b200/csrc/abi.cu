@@ -48,6 +48,7 @@ cudaError_t launch_gemm_gated(const uint8_t*, const uint16_t*, const Shape&, con
 size_t gemm_backward_workspace_bytes(int, const Shape*, int);
 cudaError_t launch_gemm_backward(int, const uint8_t* const*, const uint16_t* const*, const Shape*, const uint16_t*,
                                  int, const uint16_t* const*, uint16_t*, float* const*, void*, cudaStream_t);
+unsigned gemv_gated_error_flags();
 unsigned gemm_pair_error_flags();
 unsigned gemm_dalpha_error_flags();
 unsigned distill_error_flags();
@@ -517,11 +518,12 @@ int mbok_read_device_errors(unsigned* flags) {
   const unsigned g = gemv_lut4_error_flags();
   const unsigned m = gemm_error_flags();
   const unsigned t = gemv_mma_error_flags();
+  const unsigned d = gemv_gated_error_flags();
   const unsigned p = gemm_pair_error_flags();
   const unsigned a = gemm_dalpha_error_flags();
   const unsigned l = distill_error_flags();
-  if (g == ~0u || m == ~0u || t == ~0u || p == ~0u || a == ~0u || l == ~0u) return MBOK_ERR_CUDA;
-  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | (t ? 4u : 0u) | ((p | a) ? 8u : 0u) | (l ? 16u : 0u);
+  if (g == ~0u || m == ~0u || t == ~0u || d == ~0u || p == ~0u || a == ~0u || l == ~0u) return MBOK_ERR_CUDA;
+  *flags = (g ? 1u : 0u) | (m ? 2u : 0u) | ((t | d) ? 4u : 0u) | ((p | a) ? 8u : 0u) | (l ? 16u : 0u);
   return MBOK_OK;
 }
 

@@ -3,34 +3,42 @@
 // vector, gemv_lut.cu).
 //
 // A gated feed-forward block reads x once for two projections and uses them only
-// as this product, so neither is stored.  Each +-1 dot product of a kernel's
-// 128-column group is an exact bf16 MMA, scaled per group in fp32, as in
-// gemv_mma.cu (signs built in registers from the bits: one logic and one
-// multiply-add instruction per pair); the arrangement differs:
+// as this product, so neither is stored.  As in gemv_mma.cu each kernel's dot
+// product over a 128-column group is an exact MMA, scaled per group in fp32; the
+// rest is arranged for the instruction count, which bounds this size:
 //
+//  * Bits as they are.  A single set bit i < 10 of an fp16 word is the subnormal
+//    2^(i - 24), exact for the tensor cores.  Column i of a row's 16 is bit i of
+//    its halfword, so with bytes 0 and 1 in the two halves of a word (one byte
+//    permute) the fragment word of columns (i, i + 8) is one AND with 0x00010001
+//    << i.  The activations carry the inverse factor: 2^(7 - i) x S in fp16, S a
+//    power of two per warp and vector that puts the largest finite |x| below 2^8
+//    (exact for bf16 values down to 2^-24 of the largest, off by at most 2^-32 of
+//    it below).  With T the sum over set bits and X the sum over all columns (an
+//    MMA with every bit set, once per group), the +-1 sum is 2 T - X.  Building
+//    +-1 words took a logic and a multiply-add instruction each and more around
+//    them: 23 instructions per MMA, 35.8 us for two to eight vectors (LLaMA-7B gate
+//    and up, K = 3).
 //  * Persistent CTAs.  A warp owns at most two 128-column groups and keeps their
 //    activations in registers as MMA fragments for all rows it meets; it streams
 //    the bits and scales of its columns for one row octet after another through
-//    a private shared-memory ring (cp.async, four octets ahead).  Loading the
-//    fragments anew for every 16-row tile, on CTAs that lived for one tile, left
-//    the tensor and logic pipes idle two thirds of the time (two to eight
-//    vectors, LLaMA-7B gate and up, K = 3: 38.9 us).
-//  * An MMA's 16 rows are the 8 rows of an octet twice: the planes (matrix,
-//    kernel) of gate and up, K_gate + K_up in all, are taken two at a time, one
-//    in rows 0..7 and one in rows 8..15, so matrices with different K waste
-//    nothing (at most half an MMA).  Both halves of a fragment belong to the same
-//    octet row of the same thread.
-//  * The P warps that share a row octet (a row group; small N has several per
-//    CTA) add their columns' sums through a double-buffered shared-memory array,
-//    one barrier per octet, in warp order; two warps gate and store while the
-//    others go on.  With more columns than one CTA's warps cover (N > 5120, or
-//    4096 for more than 8 fragment columns) CTAs take slabs of columns and a
-//    second small launch adds the slabs through the workspace.
-//  * fp32 activations are split exactly into three bf16 parts (three columns).
-// What bounds it: the logic pipe.  An MMA's four fragment words take 4 logic
-// operations at half rate, about 10 cycles of a quarter SM with the unpacking of
-// the halfwords, against 8 for the MMA.
+//    a private shared-memory ring (cp.async, two to four steps ahead).
+//  * A step is two row octets (the MMA's 16 rows) with every plane (matrix,
+//    kernel) of gate and up, K_gate + K_up in all: what a step costs besides its
+//    MMAs is spread over as many as the columns give.
+//  * The P warps that share a step's rows (a row group; small N has several per
+//    CTA) leave their columns' sums in a double-buffered shared-memory array; each
+//    adds, gates and stores its share of a step's outputs, in a fixed order, one
+//    step later, when the sums have long arrived (with a barrier per step 30 % of
+//    the time passed outside the MMAs).  With
+//    more columns than one CTA's warps cover (N > 5120, or 4096 for more than 8
+//    fragment columns) CTAs take slabs of columns and a second small launch adds
+//    the slabs through the workspace.
+//  * fp32 activations are split into three fp16 parts (three columns), exact as
+//    above.
+// An infinite activation makes its vector's outputs NaN (0 x infinity in T).
 #include "lut_common.cuh"
+#include "tc_common.cuh"
 
 namespace mbok {
 
@@ -38,18 +46,25 @@ cudaError_t launch_gemv_lut_gated(const uint8_t*, const uint16_t*, const Shape&,
                                   const Shape&, const void*, bool, void*, bool, void*, cudaStream_t, bool);
 size_t gemv_gated_lut_workspace_bytes(const Shape&);
 
-constexpr int kGdDepth = 4;                  // octets in flight per warp
+constexpr int kGdMaxDepth = 4;               // steps in flight per warp: as many as fit, at least 2
+constexpr int kGdSmemMax = 227 * 1024, kGdStatic = 1024;   // of which static (barriers)
 constexpr int kGdGroups = 2;                 // groups per warp
 constexpr int kGdUnits = kGdGroups * kUnitsPerGroup;
-constexpr int kGdPlaneBytes = kGdUnits * 16;                 // one plane's bits of an octet
-constexpr int kGdAlphaBytes = kGdGroups * MBOK_MAX_K * 16;   // one matrix's scales of an octet
+constexpr int kGdPlaneBytes = 2 * kGdUnits * 16;             // one plane's bits of a step: [octet][unit][8 rows]
+constexpr int kGdScaleBytes = 2 * kGdGroups * 16;            // one plane's scales of a step: [octet][group][8 rows]
 // Warps per CTA: with one 8-column tile of vectors up to 20 (96 registers), with
 // two up to 16 (128 registers).
 template <int NT>
 struct GdGeom {
   static constexpr int kMaxWarps = NT == 1 ? 20 : 16;
-  static constexpr int kRed = 2 * 8 * NT * 8;   // floats per warp: [gate, up][column][row]
+  static constexpr int kRed = 2 * 16 * 8 * NT + 2;          // floats per warp: [gate, up][row][column], padded
+  static constexpr int kConst = (kGdGroups + 1) * 8 * NT;   // floats per warp: X of each group, 2^17 / S
 };
+// Shared memory of one warp besides its ring: two buffers of sums and constants.
+template <int NT>
+constexpr int gd_warp_bytes() { return (2 * GdGeom<NT>::kRed + GdGeom<NT>::kConst) * 4; }
+
+static __device__ unsigned int g_gemv_gated_error;
 
 struct GatedMmaParams {
   const uint8_t* packed[2];   // gate, up
@@ -62,85 +77,184 @@ struct GatedMmaParams {
   int nb;                     // vectors in this launch
   int nslab, slab_groups;     // column slabs, groups in each (fewer in the last)
   int parts, row_groups;      // warps per row group, row groups per CTA
-  int stage_bytes;
+  int stage_bytes, depth;
   int weights_static;
-  uint32_t mul[8];            // 2^(15 - 2i): sign_pair factors
 };
-
-// Bits P and P + 1 of a halfword as a bf16 pair of signs; u = h | h << 15 (see
-// gemv_mma.cu: a logic operation and a multiply-add on the FMA pipe).
-template <int P>
-__device__ __forceinline__ uint32_t gd_sign_pair(uint32_t u, const uint32_t* mul) {
-  constexpr uint32_t kMask = 0x80008000u >> (15 - P);
-  return (~u & kMask) * mul[P / 2] + 0x3F803F80u;
-}
 
 __device__ __forceinline__ void gd_mma(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Part `part` (0 = high) of the exact three-way bf16 split of v.
-__device__ __forceinline__ uint32_t gd_part(float v, int part) {
-  auto rn = [](float f) { return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(f))); };
-  const uint32_t h = rn(v);
-  if (part == 0) return h;
-  const float r = __fsub_rn(v, __uint_as_float(h << 16));
-  const uint32_t m = rn(r);
-  return part == 1 ? m : rn(__fsub_rn(r, __uint_as_float(m << 16)));
+// The same from zero.
+__device__ __forceinline__ void gd_mma0(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// The 16 activations of unit q in fragment column n as 8 bf16 pairs: vector n,
-// or part n % 3 of vector n / 3; zeros beyond the launch's vectors.
-template <bool XF32>
-__device__ __forceinline__ void gd_load_b(const GatedMmaParams& p, int n, int q, uint32_t b[8]) {
-  const int vec = XF32 ? n / 3 : n;
-  if (vec >= p.nb) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0u;
-    return;
+// The fragment word of columns (I, I + 8) from a row's 16 bits as bytes 0 and 2.
+template <int I>
+__device__ __forceinline__ uint32_t gd_word(uint32_t u) { return u & (0x00010001u << I); }
+
+// d (from zero where FIRST) += 64 columns of two planes' rows (their bits u0, u1)
+// times the fragments b.
+template <int NT, bool FIRST>
+__device__ __forceinline__ void gd_chunk(float d[NT][4], uint32_t u0, uint32_t u1, const uint32_t b[NT][8]) {
+#define MBOK_GD_STEP(J)                                                                                    \
+  _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) {                                                      \
+    if (FIRST && J == 0)                                                                                   \
+      gd_mma0(d[nt], gd_word<2 * J>(u0), gd_word<2 * J>(u1), gd_word<2 * J + 1>(u0), gd_word<2 * J + 1>(u1), \
+              b[nt][2 * J], b[nt][2 * J + 1]);                                                             \
+    else                                                                                                   \
+      gd_mma(d[nt], gd_word<2 * J>(u0), gd_word<2 * J>(u1), gd_word<2 * J + 1>(u0), gd_word<2 * J + 1>(u1), \
+             b[nt][2 * J], b[nt][2 * J + 1]);                                                              \
   }
-  if (!XF32) {
-    const uint4* src =
-        reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + size_t(vec) * p.s[0].N + q * kUnit);
-    const uint4 v0 = src[0], v1 = src[1];
-    b[0] = v0.x; b[1] = v0.y; b[2] = v0.z; b[3] = v0.w;
-    b[4] = v1.x; b[5] = v1.y; b[6] = v1.z; b[7] = v1.w;
-  } else {
-    const int part = n - 3 * vec;
-    const float4* src =
-        reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + size_t(vec) * p.s[0].N + q * kUnit);
+  MBOK_GD_STEP(0)
+  MBOK_GD_STEP(1)
+  MBOK_GD_STEP(2)
+  MBOK_GD_STEP(3)
+#undef MBOK_GD_STEP
+}
+
+// Part `part` (0 = high) of the three-way fp16 split of v.
+__device__ __forceinline__ float gd_part(float v, int part) {
+  const float h = __half2float(__float2half_rn(v));
+  if (part == 0) return h;
+  const float r = __fsub_rn(v, h);
+  const float m = __half2float(__float2half_rn(r));
+  return part == 1 ? m : __fsub_rn(r, m);
+}
+
+// The 16 activations of unit q of vector vec: raw words (8 for bf16, 16 for
+// fp32); zeros beyond the launch's vectors.
+template <bool XF32>
+struct GdUnit {
+  uint32_t w[XF32 ? 16 : 8];
+
+  __device__ __forceinline__ void load(const GatedMmaParams& p, int vec, int q) {
+    constexpr int kWords = XF32 ? 16 : 8;
+    if (vec >= p.nb) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i];
-      b[2 * i] = gd_part(v.x, part) | (gd_part(v.y, part) << 16);
-      b[2 * i + 1] = gd_part(v.z, part) | (gd_part(v.w, part) << 16);
+      for (int i = 0; i < kWords; ++i) w[i] = 0u;
+      return;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint32_t*>(p.x) +
+                                                      (size_t(vec) * p.s[0].N + q * kUnit) / (XF32 ? 1 : 2));
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = src[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
     }
   }
+  __device__ __forceinline__ float at(int i) const {
+    if (XF32) return __uint_as_float(w[i]);
+    return (i & 1) ? __uint_as_float(w[i >> 1] & 0xFFFF0000u) : __uint_as_float(w[i >> 1] << 16);
+  }
+  // The larger of m and the finite magnitudes, as fp32 bits.
+  __device__ __forceinline__ uint32_t high(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = __float_as_uint(at(i)) & 0x7FFFFFFFu;
+      if (a < 0x7F800000u) m = max(m, a);
+    }
+    return m;
+  }
+  // Fragments: column i (and i + 8) times scale times 2^(7 - i).
+  __device__ __forceinline__ void fragment(float scale, int part, uint32_t b[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f = float(1 << (7 - i));
+      float lo, hi;
+      if (XF32) {
+        lo = gd_part(at(i) * scale, part) * f;
+        hi = gd_part(at(i + 8) * scale, part) * f;
+      } else {
+        lo = at(i) * (scale * f);
+        hi = at(i + 8) * (scale * f);
+      }
+      const __half2 h = __floats2half2_rn(lo, hi);
+      b[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+};
+
+// Copy the bits (every plane, this warp's ng groups from g0) and scales of
+// octets 2 step and 2 step + 1 into a stage; one commit group.  A second octet
+// beyond the last is not copied (its rows are not stored).
+__device__ __forceinline__ void gd_issue(const GatedMmaParams& p, int step, int g0, int ng, unsigned char* st,
+                                         int lane) {
+  const int K0 = p.s[0].K, np = K0 + p.s[1].K;
+  // half a warp per octet, a lane per unit
+  const int oi = lane >> 4, u = lane & 15, o = 2 * step + oi;
+  if (o < p.s[0].O) {
+    if (u < ng * kUnitsPerGroup) {
+      unsigned char* dst = st + (oi * kGdUnits + u) * 16;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const int K = p.s[m].K;
+        const uint8_t* src = p.packed[m] + unit_offset(p.s[m], o, 0, g0 * kUnitsPerGroup + u);
+        for (int k = 0; k < K; ++k, dst += kGdPlaneBytes, src += size_t(p.s[m].Q) * 16) cp_async16(dst, src);
+      }
+    }
+    // scales: lane u takes plane u / 2, group u % 2
+    if (u < 2 * np && (u & 1) < ng) {
+      const int plane = u >> 1, g = u & 1;
+      const int m = plane < K0 ? 0 : 1, k = plane - (m != 0 ? K0 : 0);
+      cp_async16(st + np * kGdPlaneBytes + plane * kGdScaleBytes + (oi * kGdGroups + g) * 16,
+                 p.alpha[m] + alpha_offset(p.s[m], o, g0 + g, k));
+    }
+  }
+  cp_async_commit();
 }
 
-// Copy octet o's bits (every plane, this warp's ng groups from g0) and scales
-// into a stage; one commit group.
-__device__ __forceinline__ void gd_issue(const GatedMmaParams& p, int o, int g0, int ng, unsigned char* st, int lane) {
-  const int K0 = p.s[0].K, np = K0 + p.s[1].K;
-  const int per = ng * kUnitsPerGroup;   // 8 or 16 chunks per plane
-  const int shift = ng > 1 ? 4 : 3;
-  for (int c = lane; c < np * per; c += 32) {
-    const int plane = c >> shift, u = c & (per - 1);
-    const int m = plane < K0 ? 0 : 1, k = plane - (m != 0 ? K0 : 0);
-    cp_async16(st + plane * kGdPlaneBytes + u * 16, p.packed[m] + unit_offset(p.s[m], o, k, g0 * kUnitsPerGroup + u));
+// Part `part`'s share of one step's outputs (rows row0 .. row0 + 15) from the sums
+// of a row group's parts at `all` (and hi + mid + lo of fp32), added in a fixed
+// order: gated and stored, or stored for the other slabs.  With many parts four
+// lanes share an output, every fourth part each.
+template <int NT, bool XF32>
+__device__ __forceinline__ void gd_add(const GatedMmaParams& p, const float* all, int row0, int slab, int part,
+                                       int lane) {
+  using G = GdGeom<NT>;
+  const int M = p.s[0].M;
+  const int share = p.parts >= 8 ? 4 : 1, sub = lane & (share - 1);
+#pragma unroll 1
+  for (int item0 = part * (32 / share); item0 < p.nb * 16; item0 += p.parts * (32 / share)) {
+    const int item = item0 + lane / share;   // share 1: the last round may have idle lanes
+    const bool live = item < p.nb * 16;
+    const int vec = live ? item >> 4 : 0, r = item & 15;
+    float total[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float sum[XF32 ? 3 : 1];
+#pragma unroll
+      for (int q = 0; q < (XF32 ? 3 : 1); ++q) {
+        const float* at = all + (m * 16 + r) * 8 * NT + (XF32 ? 3 * vec + q : vec);
+        sum[q] = 0.f;
+        for (int w = sub; w < p.parts; w += share) sum[q] += at[w * G::kRed];
+        if (share > 1) {
+          sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 1);
+          sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], 2);
+        }
+      }
+      total[m] = XF32 ? (sum[0] + sum[XF32 ? 1 : 0]) + sum[XF32 ? 2 : 0] : sum[0];
+    }
+    if (!live || sub != 0 || row0 + r >= M) continue;
+    if (p.nslab == 1) {
+      store_act(p.h, p.h_bf16 != 0, size_t(vec) * M + row0 + r, gated(total[0], total[1]));
+    } else {
+      float* out = p.partial + (size_t(slab) * 2 * p.nb + vec) * M + row0 + r;
+      __stcg(out, total[0]);
+      __stcg(out + size_t(p.nb) * M, total[1]);
+    }
   }
-  // scales: [group][kernel][8 rows], contiguous for the warp's groups
-  unsigned char* sa = st + np * kGdPlaneBytes;
-  const int n0 = ng * K0, n1 = ng * p.s[1].K;
-  if (lane < n0) cp_async16(sa + lane * 16, p.alpha[0] + alpha_offset(p.s[0], o, g0, 0) + lane * 8);
-  else if (lane - n0 < n1)
-    cp_async16(sa + kGdAlphaBytes + (lane - n0) * 16, p.alpha[1] + alpha_offset(p.s[1], o, g0, 0) + (lane - n0) * 8);
-  cp_async_commit();
 }
 
 template <int NT, bool XF32>
@@ -151,22 +265,33 @@ gemv_gated_kernel(const __grid_constant__ GatedMmaParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, t = lane & 3;   // fragment row and column thread
   const int rg = warp / p.parts, part = warp % p.parts;
+  const int workers = p.parts * p.row_groups;
   const int slab = int(blockIdx.x) % p.nslab, cta = int(blockIdx.x) / p.nslab;
   const int ctas = (int(gridDim.x) - slab + p.nslab - 1) / p.nslab;   // CTAs of this slab
   // this warp's groups: part of the slab's, as equal as whole groups allow
   const int sg0 = slab * p.slab_groups, sg = min(p.slab_groups, p.s[0].G - sg0);
   const int g0 = sg0 + part * sg / p.parts, ng = sg0 + (part + 1) * sg / p.parts - g0;
-  const int K0 = p.s[0].K, np = K0 + p.s[1].K;
-  const int O = p.s[0].O, M = p.s[0].M;
-  unsigned char* ring = smem + warp * kGdDepth * p.stage_bytes;
-  const int warps = p.parts * p.row_groups;
-  float* red = reinterpret_cast<float*>(smem + warps * kGdDepth * p.stage_bytes);   // [2][warp][kRed]
+  const int np = p.s[0].K + p.s[1].K;
+  const int O = p.s[0].O;
+  unsigned char* ring = smem + warp * p.depth * p.stage_bytes;
+  float* red = reinterpret_cast<float*>(smem + workers * p.depth * p.stage_bytes);   // [2][worker][kRed]
+  float* consts = red + 2 * workers * G::kRed + warp * G::kConst;
+  __shared__ __align__(8) uint64_t sums_full[GdGeom<1>::kMaxWarps][2], sums_free[GdGeom<1>::kMaxWarps][2];
+  const int steps = (O + 1) / 2;
   const int first = cta * p.row_groups + rg, stride = ctas * p.row_groups;
-  const int n_mine = first < O ? (O - 1 - first) / stride + 1 : 0;
+  const int n_mine = first < steps ? (steps - 1 - first) / stride + 1 : 0;
 
+  if (threadIdx.x == 0) {
+    for (int r = 0; r < p.row_groups; ++r)
+      for (int b = 0; b < 2; ++b) {
+        tc_mbar_init(&sums_full[r][b], p.parts);
+        tc_mbar_init(&sums_free[r][b], p.parts);
+      }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  __syncthreads();
   if (p.weights_static) {
-#pragma unroll
-    for (int i = 0; i < kGdDepth; ++i) {
+    for (int i = 0; i < p.depth; ++i) {
       if (i < n_mine) gd_issue(p, first + i * stride, g0, ng, ring + i * p.stage_bytes, lane);
       else cp_async_commit();
     }
@@ -177,125 +302,127 @@ gemv_gated_kernel(const __grid_constant__ GatedMmaParams p) {
   grid_dependency_wait();
   uint32_t b[kGdGroups][2][NT][8];
 #pragma unroll
-  for (int g = 0; g < kGdGroups; ++g)
+  for (int nt = 0; nt < NT; ++nt) {
+    const int n = gq + 8 * nt, vec = XF32 ? n / 3 : n;
+    GdUnit<XF32> x[kGdGroups][2];
+    uint32_t high = 0u;   // the largest finite magnitude of the vector in this warp's columns
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int g = 0; g < kGdGroups; ++g)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (g < ng) {
-          gd_load_b<XF32>(p, gq + 8 * nt, (g0 + g) * kUnitsPerGroup + 4 * c + t, b[g][c][nt]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[g][c][nt][i] = 0u;
-        }
+      for (int c = 0; c < 2; ++c) {
+        x[g][c].load(p, g < ng ? vec : p.nb, (g0 + g) * kUnitsPerGroup + 4 * c + t);
+        high = x[g][c].high(high);
       }
-  if (!p.weights_static) {
+    high = max(high, __shfl_xor_sync(0xffffffffu, high, 1));
+    high = max(high, __shfl_xor_sync(0xffffffffu, high, 2));
+    // S = 2^e, e = 7 - floor(log2 high): at most 2^126 (tiny vectors), 1 for zeros
+    const int e = high == 0u ? 0 : min(134 - int(high >> 23), 126);
+    const float scale = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
-    for (int i = 0; i < kGdDepth; ++i) {
+    for (int g = 0; g < kGdGroups; ++g)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) x[g][c].fragment(scale, n % 3, b[g][c][nt]);
+    // 2^17 / S of the column; accumulator columns are 2t and 2t + 1
+    if (t == 0) consts[(kGdGroups * NT + nt) * 8 + gq] = __uint_as_float(uint32_t(127 - e) << 23) * 131072.f;
+  }
+  // X of each group and column: every bit set (row 0 of the product)
+#pragma unroll
+  for (int g = 0; g < kGdGroups; ++g) {
+    float d[NT][4];
+    gd_chunk<NT, true>(d, 0x00FF00FFu, 0u, b[g][0]);
+    gd_chunk<NT, false>(d, 0x00FF00FFu, 0u, b[g][1]);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      if (gq == 0) *reinterpret_cast<float2*>(consts + (g * NT + nt) * 8 + 2 * t) = make_float2(d[nt][0], d[nt][1]);
+  }
+  __syncwarp();
+  if (!p.weights_static) {
+    for (int i = 0; i < p.depth; ++i) {
       if (i < n_mine) gd_issue(p, first + i * stride, g0, ng, ring + i * p.stage_bytes, lane);
       else cp_async_commit();
     }
   }
 
-  for (int i = 0; i < n_mine; ++i) {
-    const int o = first + i * stride;
-    unsigned char* st = ring + (i % kGdDepth) * p.stage_bytes;
-    cp_async_wait<kGdDepth - 1>();   // octet i has landed (this lane's copies)
-    __syncwarp();                    // ... and every lane's
-    const unsigned char* sa = st + np * kGdPlaneBytes;
-    float y[2][NT][2];               // gate, up: row gq, columns 2t and 2t + 1 of each tile
+  bool ok = true;
+  for (int i = 0, slot = 0; i < n_mine; ++i) {
+    const int step = first + i * stride;
+    unsigned char* st = ring + slot * p.stage_bytes;
+    // the step has landed (this lane's copies)
+    if (p.depth == 4) cp_async_wait<3>();
+    else if (p.depth == 3) cp_async_wait<2>();
+    else cp_async_wait<1>();
+    __syncwarp();   // ... and every lane's
+    // gate, up: rows gq of both octets, columns 2t and 2t + 1 of each tile (as the accumulators)
+    float y[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) y[m][nt][0] = y[m][nt][1] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) y[m][nt][0] = y[m][nt][1] = y[m][nt][2] = y[m][nt][3] = 0.f;
 #pragma unroll
     for (int g = 0; g < kGdGroups; ++g) {
       if (g >= ng) break;
-      for (int q = 0; q < np; q += 2) {
-        const bool two = q + 1 < np;   // the last of an odd number of planes stands alone
-        float d[NT][4];
+      const unsigned char* bits = st + g * (kUnitsPerGroup * 16) + 16 * t + 2 * gq;
+      const unsigned char* scales = st + np * kGdPlaneBytes + g * 16 + 2 * gq;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
-        const unsigned char* bits = st + q * kGdPlaneBytes + g * (kUnitsPerGroup * 16) + 16 * t + 2 * gq;
+      for (int m = 0; m < 2; ++m) {
+        const int K = p.s[m].K;
+#pragma unroll 2
+        for (int k = 0; k < K; ++k, bits += kGdPlaneBytes, scales += kGdScaleBytes) {
+          float d[NT][4];
+          uint32_t u[2][2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint32_t h0 = *reinterpret_cast<const uint16_t*>(bits + 64 * c);
-          const uint32_t h1 = two ? *reinterpret_cast<const uint16_t*>(bits + kGdPlaneBytes + 64 * c) : 0u;
-          const uint32_t v0 = h0 | (h0 << 15), v1 = h1 | (h1 << 15);
-#define MBOK_GD_STEP(J)                                                                                            \
-  {                                                                                                                \
-    const uint32_t a0 = gd_sign_pair<4 * J>(v0, p.mul), a1 = gd_sign_pair<4 * J>(v1, p.mul);                       \
-    const uint32_t a2 = gd_sign_pair<4 * J + 2>(v0, p.mul), a3 = gd_sign_pair<4 * J + 2>(v1, p.mul);               \
-    _Pragma("unroll") for (int nt = 0; nt < NT; ++nt)                                                              \
-        gd_mma(d[nt], a0, a1, a2, a3, b[g][c][nt][2 * J], b[g][c][nt][2 * J + 1]);                                 \
-  }
-          MBOK_GD_STEP(0)
-          MBOK_GD_STEP(1)
-          MBOK_GD_STEP(2)
-          MBOK_GD_STEP(3)
-#undef MBOK_GD_STEP
-        }
-        // scale the planes' rows by the group's scales
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (e == 1 && !two) break;
-          const int plane = q + e;
-          const int m = plane < K0 ? 0 : 1, k = plane - (m != 0 ? K0 : 0);
-          const float a = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(
-              sa + m * kGdAlphaBytes + (g * p.s[m].K + k) * 16 + 2 * gq)));
+            for (int oi = 0; oi < 2; ++oi)
+              u[c][oi] = __byte_perm(*reinterpret_cast<const uint16_t*>(bits + oi * kGdUnits * 16 + 64 * c), 0u, 0x4140);
+          gd_chunk<NT, true>(d, u[0][0], u[0][1], b[g][0]);
+          gd_chunk<NT, false>(d, u[1][0], u[1][1], b[g][1]);
+          // the +-1 sums 2 T - X times the plane's group scales
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (m == 0) {
-              y[0][nt][0] = __fmaf_rn(a, d[nt][2 * e], y[0][nt][0]);
-              y[0][nt][1] = __fmaf_rn(a, d[nt][2 * e + 1], y[0][nt][1]);
-            } else {
-              y[1][nt][0] = __fmaf_rn(a, d[nt][2 * e], y[1][nt][0]);
-              y[1][nt][1] = __fmaf_rn(a, d[nt][2 * e + 1], y[1][nt][1]);
+          for (int oi = 0; oi < 2; ++oi) {
+            const float a = __half2float(
+                __ushort_as_half(*reinterpret_cast<const uint16_t*>(scales + oi * kGdGroups * 16)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 X = *reinterpret_cast<const float2*>(consts + (g * NT + nt) * 8 + 2 * t);
+              y[m][nt][2 * oi] = fmaf(a, fmaf(2.f, d[nt][2 * oi], -X.x), y[m][nt][2 * oi]);
+              y[m][nt][2 * oi + 1] = fmaf(a, fmaf(2.f, d[nt][2 * oi + 1], -X.y), y[m][nt][2 * oi + 1]);
             }
           }
         }
       }
     }
     __syncwarp();   // every lane is done with the stage
-    if (i + kGdDepth < n_mine) gd_issue(p, o + kGdDepth * stride, g0, ng, st, lane);
+    if (i + p.depth < n_mine) gd_issue(p, step + p.depth * stride, g0, ng, st, lane);
     else cp_async_commit();
-    // the row group's sums meet: [buffer][warp][gate, up][column][row]
-    float* buf = red + (i & 1) * (warps * G::kRed);
-    float* mine = buf + warp * G::kRed;
+    if (++slot == p.depth) slot = 0;
+    // this warp's sums: [buffer][warp][gate, up][column][row]
+    const int buf = i & 1;
+    if (i >= 2 && ok && !tc_wait(&sums_free[rg][buf], unsigned(i / 2 - 1) & 1u)) ok = false;
+    float* mine = red + (buf * workers + warp) * G::kRed;   // 8-byte aligned
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 back = *reinterpret_cast<const float2*>(consts + (kGdGroups * NT + nt) * 8 + 2 * t);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) mine[(m * 8 * NT + 8 * nt + 2 * t + e) * 8 + gq] = y[m][nt][e];
-    asm volatile("bar.sync %0, %1;\n" ::"r"(1 + rg), "r"(p.parts * 32) : "memory");
-    // thread (vector, row): the parts in warp order (and hi + mid + lo of fp32)
-    const float* all = buf + rg * p.parts * G::kRed;
-    for (int item = part * 32 + lane; item < p.nb * 8; item += p.parts * 32) {
-      const int vec = item >> 3, r = item & 7;
-      const int row = o * kOctet + r;
-      if (row >= M) continue;
-      float total[2];
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        float sum[XF32 ? 3 : 1];
-#pragma unroll
-        for (int q = 0; q < (XF32 ? 3 : 1); ++q) {
-          const float* at = all + (m * 8 * NT + (XF32 ? 3 * vec + q : vec)) * 8 + r;
-          sum[q] = 0.f;
-          for (int w = 0; w < p.parts; ++w) sum[q] += at[w * G::kRed];
-        }
-        total[m] = XF32 ? (sum[0] + sum[XF32 ? 1 : 0]) + sum[XF32 ? 2 : 0] : sum[0];
-      }
-      if (p.nslab == 1) {
-        store_act(p.h, p.h_bf16 != 0, size_t(vec) * M + row, gated(total[0], total[1]));
-      } else {
-        float* out = p.partial + (size_t(slab) * 2 * p.nb + vec) * M + row;
-        __stcg(out, total[0]);
-        __stcg(out + size_t(p.nb) * M, total[1]);
-      }
+        for (int oi = 0; oi < 2; ++oi)
+          *reinterpret_cast<float2*>(mine + (m * 16 + 8 * oi + gq) * 8 * NT + 8 * nt + 2 * t) =
+              make_float2(y[m][nt][2 * oi] * back.x, y[m][nt][2 * oi + 1] * back.y);
+    }
+    __syncwarp();
+    if (lane == 0) tc_arrive(&sums_full[rg][buf]);
+    // this warp's share of step i - 1 (and at the end of the last step)
+    for (int j = i > 0 ? i - 1 : i; j <= (i + 1 < n_mine ? i - 1 : i); ++j) {
+      if (ok && !tc_wait(&sums_full[rg][j & 1], unsigned(j / 2) & 1u)) ok = false;
+      if (!ok) continue;   // nothing more is stored
+      gd_add<NT, XF32>(p, red + ((j & 1) * workers + rg * p.parts) * G::kRed, (first + j * stride) * 2 * kOctet, slab,
+                       part, lane);
+      __syncwarp();
+      if (lane == 0) tc_arrive(&sums_free[rg][j & 1]);
     }
   }
+  if (!ok) atomicOr(&g_gemv_gated_error, 1u);
   cp_async_wait<0>();
 }
 
@@ -336,7 +463,7 @@ static GdPlan gd_plan(int groups, int max_warps) {
   pl.nslab = (groups + pl.slab_groups - 1) / pl.slab_groups;
   pl.parts = (pl.slab_groups + kGdGroups - 1) / kGdGroups;
   pl.row_groups = max_warps / pl.parts;
-  if (pl.row_groups > 8) pl.row_groups = 8;   // a named barrier each
+  if (pl.row_groups > 8) pl.row_groups = 8;
   return pl;
 }
 
@@ -368,16 +495,20 @@ static cudaError_t launch_gd(GatedMmaParams& p, cudaStream_t stream) {
   p.slab_groups = pl.slab_groups;
   p.parts = pl.parts;
   p.row_groups = pl.row_groups;
-  p.stage_bytes = (p.s[0].K + p.s[1].K) * kGdPlaneBytes + 2 * kGdAlphaBytes;
-  constexpr int kStageMax = 2 * MBOK_MAX_K * kGdPlaneBytes + 2 * kGdAlphaBytes;
-  constexpr int kSmemMax = G::kMaxWarps * (kGdDepth * kStageMax + 2 * G::kRed * 4);
-  static_assert(kSmemMax <= 227 * 1024, "the ring and the sums fit one CTA");
+  p.stage_bytes = (p.s[0].K + p.s[1].K) * (kGdPlaneBytes + kGdScaleBytes);
+  const int workers = pl.parts * pl.row_groups;
+  const int red_bytes = workers * gd_warp_bytes<NT>();
+  p.depth = (kGdSmemMax - kGdStatic - red_bytes) / (workers * p.stage_bytes);
+  if (p.depth > kGdMaxDepth) p.depth = kGdMaxDepth;
+  static_assert(G::kMaxWarps * (2 * 2 * MBOK_MAX_K * (kGdPlaneBytes + kGdScaleBytes) + gd_warp_bytes<NT>()) <=
+                    kGdSmemMax - kGdStatic,
+                "two steps and the sums fit one CTA");
   auto fn = gemv_gated_kernel<NT, XF32>;
   static PerDeviceOnce attr_once;   // the attribute is per device context
-  const cudaError_t ae = set_smem_attr_once(attr_once, reinterpret_cast<const void*>(fn), kSmemMax);
+  const cudaError_t ae = set_smem_attr_once(attr_once, reinterpret_cast<const void*>(fn), kGdSmemMax - kGdStatic);
   if (ae != cudaSuccess) return ae;
-  const int warps = pl.parts * pl.row_groups;
-  const int per_slab = (p.s[0].O + pl.row_groups - 1) / pl.row_groups;   // CTAs that have an octet to begin with
+  const int steps = (p.s[0].O + 1) / 2;
+  const int per_slab = (steps + pl.row_groups - 1) / pl.row_groups;   // CTAs that have a step to begin with
   int ctas = device_sm_count() / pl.nslab;
   if (ctas < 1) ctas = 1;
   if (ctas > per_slab) ctas = per_slab;
@@ -386,8 +517,8 @@ static cudaError_t launch_gd(GatedMmaParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas * pl.nslab);
-  cfg.blockDim = dim3(warps * 32);
-  cfg.dynamicSmemBytes = size_t(warps) * (kGdDepth * p.stage_bytes + 2 * G::kRed * 4);
+  cfg.blockDim = dim3(workers * 32);
+  cfg.dynamicSmemBytes = size_t(workers * p.depth * p.stage_bytes + red_bytes);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -433,13 +564,21 @@ cudaError_t launch_gemv_gated(const uint8_t* packed_gate, const uint16_t* alpha_
     p.partial = static_cast<float*>(workspace);
     p.nb = batch - b0 < per_launch ? batch - b0 : per_launch;
     p.weights_static = weights_static ? 1 : 0;
-    for (int i = 0; i < 8; ++i) p.mul[i] = 1u << (15 - 2 * i);
     const bool one = gd_columns(x_f32, p.nb) <= 8;
     const cudaError_t e = one ? (x_f32 ? launch_gd<1, true>(p, stream) : launch_gd<1, false>(p, stream))
                               : (x_f32 ? launch_gd<2, true>(p, stream) : launch_gd<2, false>(p, stream));
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+// Reads and clears the kernel's error flag; ~0u if the read itself failed.
+unsigned gemv_gated_error_flags() {
+  unsigned v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_gemv_gated_error, sizeof(v)) != cudaSuccess) return ~0u;
+  const unsigned z = 0;
+  if (v != 0 && cudaMemcpyToSymbol(g_gemv_gated_error, &z, sizeof(z)) != cudaSuccess) return ~0u;
+  return v;
 }
 
 }  // namespace mbok

@@ -35,11 +35,12 @@ __device__ __forceinline__ void tc_arrive_expect_tx(uint64_t* bar, unsigned byte
                : "memory");
 }
 
-// Bounded wait for phase `parity`; false on timeout.
+// Bounded wait for phase `parity`; false on timeout.  The time is looked at once
+// in 256 tries, not on the first: reading it costs far more than a try.
 __device__ __forceinline__ bool tc_wait(uint64_t* bar, unsigned parity, unsigned long long limit = kTcWaitNs) {
   const uint32_t a = tc_smem(bar);
   unsigned long long t0 = 0;
-  for (unsigned it = 0;; ++it) {
+  for (unsigned it = 1;; ++it) {
     uint32_t done;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"

@@ -43,8 +43,7 @@ __device__ __forceinline__ void pair_tma_load_2d(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// As tc_wait, ordered after arrivals from either CTA.  The time is looked at
-// once in 256 tries, not on the first: reading it costs far more than a try.
+// As tc_wait, ordered after arrivals from either CTA.
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, unsigned parity, unsigned long long limit = kTcWaitNs) {
   const uint32_t a = tc_smem(bar);
   unsigned long long t0 = 0;
