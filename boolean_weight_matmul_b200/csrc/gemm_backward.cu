@@ -8,7 +8,7 @@ namespace mbok {
 cudaError_t launch_gemm_grad_x(int, const uint8_t* const*, const uint16_t* const*, const Shape*,
                                const uint16_t* const*, const int*, const float*, int, uint16_t*, cudaStream_t);
 cudaError_t launch_gemm_dalpha(int, const uint8_t* const*, const Shape*, const uint16_t*, int, const uint16_t* const*,
-                               const int*, float* const*, int, void*, cudaStream_t);
+                               const int*, float* const*, int, bool, void*, cudaStream_t);
 int dalpha_splits(int, const Shape*, int);
 size_t dalpha_workspace_bytes(int, const Shape*, int);
 
@@ -91,7 +91,7 @@ cudaError_t launch_gemm_backward(int nmat, const uint8_t* const* packed, const u
     e = launch_gemm_grad_x(nmat, packed, alpha, shapes, scaled, pl.ld, inverse, T, dX, stream);
   if (e == cudaSuccess && nd > 0)
     e = launch_gemm_dalpha(nd, d_packed, d_shapes, X, T, d_dy, d_ld, d_out, dalpha_splits(nmat, shapes, T),
-                           ws + pl.splits, stream);
+                           dX != nullptr, ws + pl.splits, stream);
   return e;
 }
 

@@ -67,6 +67,7 @@ struct DaParams {
   int stages;           // token stages in all
   size_t split_stride;  // floats between the splits' outputs
   uint32_t idesc;
+  int beside;           // follows the input gradient's kernel, of which it needs nothing
 };
 
 struct DaItem {
@@ -175,6 +176,10 @@ gemm_dalpha_kernel(const __grid_constant__ DaMaps maps, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+  // Behind the input gradient's kernel (which starts this one once all before it
+  // is complete) this one runs beside it, and waits for it only at its end.
+  if (!p.beside) pdl_wait();
+  pdl_launch();
 
   if (warp == 0) {
     // ---- TMA producer: 128 rows of dY^T and half of the tile's columns of X ----
@@ -294,6 +299,7 @@ gemm_dalpha_kernel(const __grid_constant__ DaMaps maps, const __grid_constant__ 
     tc_fence_after();
     pair_dealloc(tmem, kDaTmemCols);
   }
+  if (p.beside) pdl_wait();   // this grid's completion stands for both
 }
 
 // out[i] = the splits' sums in order; the matrices' regions follow one another
@@ -306,6 +312,8 @@ struct DaJoin {
 
 __global__ void __launch_bounds__(256) dalpha_join_kernel(const float* part, size_t split_stride, int splits,
                                                           const __grid_constant__ DaJoin j) {
+  pdl_launch();
+  pdl_wait();
   const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= j.first[j.nmat]) return;
   float4 sum = __ldcs(reinterpret_cast<const float4*>(part) + i);
@@ -380,10 +388,11 @@ static int da_pair_count() {
 
 // dalpha_s for nmat matrices (dY_s bf16 with rows ld[s] apart, a multiple of 8).
 // splits: dalpha_splits of these matrices or of a set that holds them;
+// beside: the launch before it in the stream is launch_gemm_grad_x's.
 // workspace as sized by dalpha_workspace_bytes for that set, 16-byte aligned.
 cudaError_t launch_gemm_dalpha(int nmat, const uint8_t* const* packed, const Shape* shapes, const uint16_t* X, int T,
                                const uint16_t* const* dys, const int* ld, float* const* dalpha, int splits,
-                               void* workspace, cudaStream_t stream) {
+                               bool beside, void* workspace, cudaStream_t stream) {
   const int pairs = da_pair_count();
   if (pairs < 1) return cudaErrorNotSupported;
   DaMaps maps;
@@ -422,12 +431,12 @@ cudaError_t launch_gemm_dalpha(int nmat, const uint8_t* const* packed, const Sha
   if (!good) return cudaErrorInvalidValue;
   const long items = long(p.ntiles) * p.splits;
   const int grid = 2 * int(items < pairs ? items : pairs);
-  gemm_dalpha_kernel<<<grid, kDaThreads, kDaSmem, stream>>>(maps, p);
-  const cudaError_t e = cudaGetLastError();
+  p.beside = beside ? 1 : 0;
+  const cudaError_t e =
+      launch_dependent(gemm_dalpha_kernel, dim3(grid), dim3(kDaThreads), size_t(kDaSmem), stream, maps, p);
   if (e != cudaSuccess || p.splits == 1) return e;
-  dalpha_join_kernel<<<unsigned((off / 4 + 255) / 256), 256, 0, stream>>>(static_cast<const float*>(workspace), off,
-                                                                         p.splits, join);
-  return cudaGetLastError();
+  return launch_dependent(dalpha_join_kernel, dim3(unsigned((off / 4 + 255) / 256)), dim3(256), 0, stream,
+                          static_cast<const float*>(workspace), off, p.splits, join);
 }
 
 }  // namespace mbok

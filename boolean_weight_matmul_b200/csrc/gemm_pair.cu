@@ -353,6 +353,10 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
+  // What is above overlaps the preceding grid.  The scale gradients' kernel that
+  // may follow reads nothing that this one writes: it may start on idle SMs.
+  pdl_wait();
+  pdl_launch();
 
   // Every role walks the stages of all its tiles with a slot index and the
   // parity of the slot's current use.
@@ -610,8 +614,7 @@ static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t
   for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
   const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
   const int grid = 2 * (p.ntiles < pairs ? p.ntiles : pairs);
-  gemm_pair_kernel<MODE><<<grid, kPairThreads, smem, stream>>>(maps, p);
-  return cudaGetLastError();
+  return launch_dependent(gemm_pair_kernel<MODE>, dim3(grid), dim3(kPairThreads), size_t(smem), stream, maps, p);
 }
 
 static void set_tokens(PairParams& p, int n) {

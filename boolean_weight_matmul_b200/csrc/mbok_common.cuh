@@ -66,6 +66,30 @@ __device__ __forceinline__ void store_act(void* out, bool bf16, size_t i, float 
   else static_cast<float*>(out)[i] = v;
 }
 
+// Programmatic dependent launch: return once the preceding grid of the stream is
+// complete; let the following grid start.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// A launch that may start while the preceding grid of the stream runs (the
+// kernel waits for it with pdl_wait before it touches what that grid may write
+// or read).
+template <class... Params, class... Args>
+inline cudaError_t launch_dependent(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                    const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<Params>(args)...);
+}
+
 // The current device index, or -1 if the runtime cannot say.
 inline int current_device() {
   int dev = -1;

@@ -42,6 +42,8 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t pair, float f) {
 __global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_constant__ ScaleRows p) {
   __shared__ uint32_t warp_max[kScaleThreads / 32];
   const size_t t = blockIdx.x;
+  pdl_launch();
+  pdl_wait();   // the sources, and the workspace of an earlier call
   uint32_t m = 0;
   for (int s = 0; s < p.nseg; ++s) {
     const ScaleSeg& g = p.seg[s];
@@ -76,8 +78,7 @@ __global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_
 }
 
 cudaError_t launch_scale_rows(const ScaleRows& p, int T, cudaStream_t stream) {
-  scale_rows_kernel<<<unsigned(T), kScaleThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(scale_rows_kernel, dim3(unsigned(T)), dim3(kScaleThreads), 0, stream, p);
 }
 
 }  // namespace mbok
