@@ -41,7 +41,7 @@ cudaError_t launch_gemv_gated(const uint8_t*, const uint16_t*, const Shape&, con
                               const Shape&, const void*, bool, int, void*, bool, void*, cudaStream_t, bool);
 cudaError_t launch_gated_backward(const uint16_t*, const uint16_t*, const uint16_t*, size_t, uint16_t*, uint16_t*,
                                   uint16_t*, cudaStream_t);
-size_t gemm_gated_workspace_bytes(int, int);
+size_t gemm_gated_workspace_bytes(int, int, int);
 cudaError_t launch_gemm_gated(const uint8_t*, const uint16_t*, const Shape&, const uint8_t*, const uint16_t*,
                               const Shape&, const uint16_t*, int, uint16_t*, uint16_t*, uint16_t*, void*,
                               cudaStream_t);
@@ -363,7 +363,7 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
 
 size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T) {
   if (check_shape(1, M, N) != MBOK_OK || T < 1 || T > kMaxTokens) return 0;
-  return gemm_gated_workspace_bytes(N, T);
+  return gemm_gated_workspace_bytes(M, N, T);
 }
 
 int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
@@ -380,7 +380,7 @@ int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int
   if (!aligned(packed_gate, 16) || !aligned(alpha_gate, 16) || !aligned(packed_up, 16) || !aligned(alpha_up, 16) ||
       !aligned(X, 16) || !aligned(H, 16) || !aligned(gate, 16) || !aligned(up, 16))
     return MBOK_ERR_ALIGN;
-  if (workspace == nullptr || workspace_bytes < gemm_gated_workspace_bytes(N, T) || !aligned(workspace, 256))
+  if (workspace == nullptr || workspace_bytes < gemm_gated_workspace_bytes(M, N, T) || !aligned(workspace, 256))
     return MBOK_ERR_WORKSPACE;
   return from_cuda(launch_gemm_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate,
                                      make_shape(K_gate, M, N), reinterpret_cast<const uint8_t*>(packed_up), alpha_up,

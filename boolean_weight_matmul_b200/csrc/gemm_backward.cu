@@ -6,7 +6,8 @@
 namespace mbok {
 
 cudaError_t launch_gemm_grad_x(int, const uint8_t* const*, const uint16_t* const*, const Shape*,
-                               const uint16_t* const*, const int*, const float*, int, uint16_t*, cudaStream_t);
+                               const uint16_t* const*, const int*, const float*, int, uint16_t*, void*, cudaStream_t);
+size_t gemm_grad_x_workspace_bytes(int, const Shape*, int);
 cudaError_t launch_gemm_dalpha(int, const uint8_t* const*, const Shape*, const uint16_t*, int, const uint16_t* const*,
                                const int*, float* const*, int, bool, void*, cudaStream_t);
 int dalpha_splits(int, const Shape*, int);
@@ -20,7 +21,7 @@ struct Plan {
   size_t scaled[kMaxMats];       // fp16 [T][ld]
   size_t copy[kMaxMats];         // bf16 [T][ld] where M is not a multiple of 8 (TMA rows are 16-byte aligned)
   size_t inverse;                // fp32 [T rounded up to 16]
-  size_t splits;                 // the scale gradients' partial sums
+  size_t splits, splits_x;       // the scale gradients' and dX's partial sums
   size_t total;
 };
 
@@ -39,6 +40,7 @@ Plan make_plan(int nmat, const Shape* shapes, int T) {
   }
   pl.inverse = take((size_t(T) + 15) / 16 * 16 * sizeof(float));
   pl.splits = take(dalpha_workspace_bytes(nmat, shapes, T));
+  pl.splits_x = take(gemm_grad_x_workspace_bytes(nmat, shapes, T));
   pl.total = at;
   return pl;
 }
@@ -88,7 +90,7 @@ cudaError_t launch_gemm_backward(int nmat, const uint8_t* const* packed, const u
   }
   cudaError_t e = pass ? launch_scale_rows(sc, T, stream) : cudaSuccess;
   if (e == cudaSuccess && dX != nullptr)
-    e = launch_gemm_grad_x(nmat, packed, alpha, shapes, scaled, pl.ld, inverse, T, dX, stream);
+    e = launch_gemm_grad_x(nmat, packed, alpha, shapes, scaled, pl.ld, inverse, T, dX, ws + pl.splits_x, stream);
   if (e == cudaSuccess && nd > 0)
     e = launch_gemm_dalpha(nd, d_packed, d_shapes, X, T, d_dy, d_ld, d_out, dalpha_splits(nmat, shapes, T),
                            dX != nullptr, ws + pl.splits, stream);

@@ -40,6 +40,8 @@
 // stage to both CTAs' `empty` barriers.  Four epilogue warps, one per
 // tensor-memory lane quarter, drain finished tiles; the unpack warps join them
 // for a CTA's last tile and for every two-accumulator tile.
+// With few tiles the contraction is split over several pairs, which leave fp32
+// sums in the workspace; a second kernel adds them in order (and gates).
 // Every mbarrier wait is bounded (1 s): on timeout the CTA records an error
 // flag, drains what it issued (bounded) and leaves with the other.
 #include "scale_rows.h"
@@ -99,13 +101,29 @@ struct PairParams {
   int stages;          // per tile
   int row_tiles;       // tiles along W's rows (GATE, 128) or columns (GRAD, 256)
   int ntiles;
+  int splits, nitems;  // parts of the contraction; tiles x splits
   uint32_t idesc;
   PairMul mul;
   const float* inverse;   // [T rounded up to 16]
   uint16_t* out;          // H, or dX
   uint16_t* gate;         // GATE: [T][M] or nullptr
   uint16_t* up;
+  float* partial;         // several splits: GRAD [split][T][N], GATE [split][gate, up][T][M]
 };
+
+// Item i of a launch: a tile and its part of the contraction (splits vary
+// slowest, then token tiles: pairs that run together share their tokens).
+struct PairItem {
+  int tile, split, k0, k1;
+};
+__device__ __forceinline__ PairItem pair_item(const PairParams& p, int i) {
+  PairItem it;
+  it.split = i / p.ntiles;
+  it.tile = i - it.split * p.ntiles;
+  it.k0 = int(long(it.split) * p.stages / p.splits);
+  it.k1 = int(long(it.split + 1) * p.stages / p.splits);
+  return it;
+}
 
 // ---- unpack ----
 //
@@ -265,11 +283,11 @@ __device__ __forceinline__ float gated_fast(float g, float u) { return __fdivide
 // Drain one warp's share of a finished tile whose first accumulator is at
 // `tmem`: lane quarter q, chunks of 16 tokens first, first + stride, ...
 template <PairMode MODE>
-__device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, int tile, int rank, int q, int lane,
-                                           int first, int stride) {
+__device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, const PairItem& it, int rank, int q,
+                                           int lane, int first, int stride) {
   const int per = p.n_acc / 16;
-  const int t0 = (tile / p.row_tiles) * p.n;
-  const int rt = tile % p.row_tiles;
+  const int t0 = (it.tile / p.row_tiles) * p.n;
+  const int rt = it.tile % p.row_tiles;
   const int rows = MODE == kGate ? p.M : p.N;
   const bool pairs = rows % 2 == 0;   // every buffer is 16-byte aligned
   const int r = MODE == kGate ? rt * 128 + rank * 64 + 16 * q + (lane & 15) : rt * 256 + rank * 128 + 32 * q + lane;
@@ -288,7 +306,15 @@ __device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, i
       v[4 * i + 2] = __uint_as_float(w[4 * i + 2]) * s.z;
       v[4 * i + 3] = __uint_as_float(w[4 * i + 3]) * s.w;
     }
-    if (MODE == kGrad) {
+    if (p.splits > 1) {
+      if (r < rows) {
+        const size_t plane = MODE == kGate ? size_t(2 * it.split + (lane >> 4)) : size_t(it.split);
+        float* at = p.partial + (plane * p.T + t) * rows + r;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, at += rows)
+          if (t + i < p.T) __stcg(at, v[i]);
+      }
+    } else if (MODE == kGrad) {
       store_rows<16>(pairs, p.out, rows, rows, p.T, r, t, v, lane);
     } else {
       const bool low = lane < 16;
@@ -328,7 +354,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(pair_rank());
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int n_mine = (p.ntiles - 1 - pair) / npairs + 1;   // tiles pair, pair + npairs, ...; at least one
+  const int n_mine = (p.nitems - 1 - pair) / npairs + 1;   // items pair, pair + npairs, ...; at least one
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairMaxSlots; ++s) {
@@ -365,10 +391,13 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     const unsigned bytes = unsigned(p.n * kPairBK * 2);   // both CTAs'
     int s = 0, g = 0;
     unsigned ph = 1;   // parity of the slot's previous use
-    for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
-      const int t0 = (tile / p.row_tiles) * p.n + rank * (p.n_acc / 2);
-      int m = 0, step = 0;   // GRAD: matrix and its 64-row step
-      for (int kb = 0; kb < p.stages; ++kb, ++g) {
+    for (int i = 0; i < n_mine && ok; ++i) {
+      const PairItem it = pair_item(p, pair + i * npairs);
+      const int t0 = (it.tile / p.row_tiles) * p.n + rank * (p.n_acc / 2);
+      int m = 0, step = it.k0;   // GRAD: matrix and its 64-row step
+      if (MODE == kGrad)
+        while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
+      for (int kb = it.k0; kb < it.k1; ++kb, ++g) {
         if (g >= p.slots && !pair_wait(&empty[s], ph)) { ok = false; break; }
         const uint32_t bar = pair_leader(&ready[s]);
         const CUtensorMap* map = &maps.act[MODE == kGate ? 0 : m];
@@ -388,10 +417,13 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     // ---- copies of bits and scales ----
     int s = 0, g = 0;
     unsigned ph = 1;
-    for (int tile = pair; tile < p.ntiles && ok; tile += npairs) {
-      const int rt = tile % p.row_tiles;
-      int m = 0, step = 0;
-      for (int kb = 0; kb < p.stages; ++kb, ++g) {
+    for (int i = 0; i < n_mine && ok; ++i) {
+      const PairItem it = pair_item(p, pair + i * npairs);
+      const int rt = it.tile % p.row_tiles;
+      int m = 0, step = it.k0;
+      if (MODE == kGrad)
+        while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
+      for (int kb = it.k0; kb < it.k1; ++kb, ++g) {
         if (g >= p.wslots && !pair_wait(&wempty[s], ph)) { ok = false; break; }
         unsigned char* w = wring + s * kPairWBytes;
         if (MODE == kGate) {
@@ -434,7 +466,8 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         if (use > 0 && !pair_wait(&tempty[b], unsigned(use - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(b * 256);
-        for (int kb = 0; kb < p.stages; ++kb) {
+        const PairItem it = pair_item(p, pair + i * npairs);
+        for (int kb = it.k0; kb < it.k1; ++kb) {
           if (!pair_wait(&ready[s], ph)) { ok = false; break; }
           tc_fence_after();
           const uint64_t off = uint64_t((s * slot_bytes) >> 4);
@@ -442,12 +475,12 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < kPairBK / 16; ++kk) {
               const uint64_t ad = a0 + off + uint64_t(kk * kAStep), xd = x0 + off + uint64_t(kk * (32 >> 4));
-              const uint32_t acc = (kb > 0 || kk > 0) ? 1u : 0u;
+              const uint32_t acc = (kb > it.k0 || kk > 0) ? 1u : 0u;
               pair_mma(d, ad, xd, p.idesc, acc);
               if (p.naccs > 1) pair_mma(d + 256, ad, xd + uint64_t(x_bytes >> 4), p.idesc, acc);
             }
             pair_commit(&empty[s]);
-            if (kb + 1 == p.stages) {
+            if (kb + 1 == it.k1) {
               pair_commit(&tfull[b]);
               if (i + 1 == n_mine) pair_commit(last_full);
             }
@@ -464,9 +497,9 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     int s = grp, ws = grp, g = grp, first = grp;   // both rings have at least kPairGroups slots
     unsigned ph = 0, wph = 0;
     for (int i = 0; i < n_mine && ok; ++i) {
-      int m = 0, step = first;
-      int kb = first;
-      for (; kb < p.stages; kb += kPairGroups, step += kPairGroups, g += kPairGroups) {
+      const PairItem it = pair_item(p, pair + i * npairs);
+      int m = 0, kb = it.k0 + first, step = kb;
+      for (; kb < it.k1; kb += kPairGroups, step += kPairGroups, g += kPairGroups) {
         const unsigned char* w = wring + ws * kPairWBytes;
         unsigned char* a = smem + s * slot_bytes;
         // the bits are there, and the slot's previous MMAs are done with its A
@@ -497,7 +530,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         if ((s += kPairGroups) >= p.slots) { s -= p.slots; ph ^= 1u; }
         if ((ws += kPairGroups) >= p.wslots) { ws -= p.wslots; wph ^= 1u; }
       }
-      first = kb - p.stages;   // this group's first stage of the next tile
+      first = kb - it.k1;   // this group's first stage of the next item
       if (!ok) break;
       // Two accumulators: every tile is drained by all warps.  One: only the
       // last tile, on a barrier that completes once (a parity wait on tfull from
@@ -508,7 +541,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         if (!(p.naccs > 1 ? pair_wait(&tfull[0], unsigned(i) & 1u) : pair_wait(last_full, 0u))) { ok = false; break; }
         tc_fence_after();
         const int b = p.naccs > 1 ? 0 : i & 1;
-        pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair + i * npairs, rank, warp & 3, lane,
+        pair_drain<MODE>(p, tmem + uint32_t(b * 256), it, rank, warp & 3, lane,
                          1 + (warp - kPairUnpackWarp0) / 4, 1 + kPairUnpackWarps / 4);
         tc_fence_before();
         __syncwarp();
@@ -522,7 +555,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       if (!pair_wait(&tfull[b], unsigned(use) & 1u)) { ok = false; break; }
       tc_fence_after();
       const bool shared = p.naccs > 1 || i + 1 == n_mine;   // with the unpack warps: every fifth chunk
-      pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair + i * npairs, rank, warp & 3, lane, 0,
+      pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair_item(p, pair + i * npairs), rank, warp & 3, lane, 0,
                        shared ? 1 + kPairUnpackWarps / 4 : 1);
       tc_fence_before();
       __syncwarp();
@@ -544,6 +577,54 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   if (warp == 1) {
     tc_fence_after();
     pair_dealloc(tmem, kPairTmemCols);
+  }
+}
+
+// dX, or H (and G and U), from the splits' sums in order; n = T x rows, 4 values
+// per thread where n allows.
+template <PairMode MODE>
+__global__ void __launch_bounds__(256) pair_join_kernel(const float* part, int splits, size_t n, uint16_t* out,
+                                                        uint16_t* gate, uint16_t* up) {
+  pdl_launch();
+  pdl_wait();
+  const size_t i0 = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i0 >= n) return;
+  const bool vec = n % 4 == 0;   // every plane 16-byte aligned
+  constexpr int kPlanes = MODE == kGate ? 2 : 1;
+  float sum[kPlanes][4] = {};
+  for (int s = 0; s < splits; ++s)
+#pragma unroll
+    for (int m = 0; m < kPlanes; ++m) {
+      const float* at = part + (size_t(s) * kPlanes + m) * n + i0;
+      if (vec) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(at));
+        sum[m][0] += v.x; sum[m][1] += v.y; sum[m][2] += v.z; sum[m][3] += v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i0 + e < n) sum[m][e] += __ldcg(at + e);
+      }
+    }
+  auto store = [&](uint16_t* to, const float* v) {
+    if (vec) {
+      *reinterpret_cast<uint2*>(to + i0) = make_uint2(tc_pack_bf16x2(v[0], v[1]), tc_pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i0 + e < n) to[i0 + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+    }
+  };
+  if (MODE == kGrad) {
+    store(out, sum[0]);
+  } else {
+    if (gate != nullptr) {
+      store(gate, sum[0]);
+      store(up, sum[kPlanes - 1]);
+    }
+    float h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = gated_fast(sum[0][e], sum[kPlanes - 1][e]);
+    store(out, h);
   }
 }
 
@@ -583,21 +664,42 @@ static int pair_count() {
   });
 }
 
-// Tokens per tile (a multiple of 32, at most 512) that minimises the time of
-// the wave-quantised grid.  A stage costs its tokens' MMAs, and at least the
-// unpack of its weights (about 320 tokens' worth); a tile of more than 256
-// tokens adds its drain, about 10 stages' worth.
-static int pair_token_tile(int row_tiles, int stages, int T, int pairs) {
-  if (pairs < 1) pairs = 1;
-  int best = 512;
+// Tokens per tile and splits of the contraction.
+struct PairPlan {
+  int n, splits;
+};
+
+// Tiles of n tokens (a multiple of 32, at most 512) and splits that minimise the
+// time of the wave-quantised grid of kPlanPairs pairs (the plan does not ask the
+// device, so that a workspace's size does not depend on it).  In units of one
+// token's MMAs of a stage (about 1.1 ns): a stage costs its tokens, and at least
+// the unpack of its weights (320 tokens' worth); an item adds its pipeline's fill
+// and what of its drain is not hidden (4 stages, 12 with two accumulators);
+// splits add their sums' way through memory (at 5 TB/s) and a launch (2 us).
+// Measured: dX of 9998 x 896, K = 2, 32 tokens 66.8 us unsplit; gated 389 rows,
+// N = 3456, 1027 tokens 32.6 us.
+constexpr int kPlanPairs = 74;
+constexpr int kPairMaxSplits = 16;
+static PairPlan pair_plan(int row_tiles, int stages, int T, long out_floats) {
+  PairPlan best = {512, 1};
   double best_cost = -1;
   const int most = T >= 512 ? 512 : (T + 31) / 32 * 32;
-  for (int n = most; n >= 32; n -= 32) {
+  static const int kWidths[] = {512, 448, 416, 384, 352, 320, 288, 256, 224, 192, 160, 128, 96, 64, 32};
+  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kPairMaxSplits};
+  for (const int n : kWidths) {
+    if (n > most) continue;
     const long tiles = long(row_tiles) * ((T + n - 1) / n);
-    const double cost = double((tiles + pairs - 1) / pairs) * (n > 320 ? n : 320) * (stages + (n > 256 ? 10 : 0));
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = n;
+    for (const int s : kSplits) {
+      if (s > 1 && (s * 4 > stages + 3 || tiles * s > 8 * kPlanPairs)) break;   // short parts, or the grid is full
+      const double waves = double((tiles * s + kPlanPairs - 1) / kPlanPairs);
+      const double per_item = double((stages + s - 1) / s) + (n > 256 ? 12 : 4);
+      double cost = waves * (n > 320 ? n : 320) * per_item;
+      if (s > 1) cost += (8.0 * s * double(out_floats) / 5000.0 + 2000.0) / 1.1;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best.n = n;
+        best.splits = s;
+      }
     }
   }
   return best;
@@ -613,15 +715,22 @@ static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t
   p.wslots = wslots < kPairMaxSlots ? wslots : kPairMaxSlots;
   for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
   const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
-  const int grid = 2 * (p.ntiles < pairs ? p.ntiles : pairs);
-  return launch_dependent(gemm_pair_kernel<MODE>, dim3(grid), dim3(kPairThreads), size_t(smem), stream, maps, p);
+  const int grid = 2 * (p.nitems < pairs ? p.nitems : pairs);
+  const cudaError_t e =
+      launch_dependent(gemm_pair_kernel<MODE>, dim3(grid), dim3(kPairThreads), size_t(smem), stream, maps, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const size_t n = size_t(p.T) * (MODE == kGate ? p.M : p.N);
+  return launch_dependent(pair_join_kernel<MODE>, dim3(unsigned((n + 1023) / 1024)), dim3(256), 0, stream,
+                          static_cast<const float*>(p.partial), p.splits, n, p.out, p.gate, p.up);
 }
 
-static void set_tokens(PairParams& p, int n) {
-  p.n = n;
-  p.naccs = n > 256 ? 2 : 1;
-  p.n_acc = n / p.naccs;   // n is a multiple of 32
-  p.ntiles = p.row_tiles * ((p.T + n - 1) / n);
+static void set_plan(PairParams& p, const PairPlan& pl) {
+  p.n = pl.n;
+  p.naccs = p.n > 256 ? 2 : 1;
+  p.n_acc = p.n / p.naccs;   // n is a multiple of 32
+  p.ntiles = p.row_tiles * ((p.T + p.n - 1) / p.n);
+  p.splits = pl.splits;
+  p.nitems = p.ntiles * p.splits;
 }
 
 static size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -629,8 +738,15 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // ---- gated forward ----
 
-size_t gemm_gated_workspace_bytes(int N, int T) {
-  return up256(size_t(T) * N * 2) + up16(T) * sizeof(float);
+static PairPlan gate_plan(int M, int N, int T) {
+  return pair_plan((M + 127) / 128, N / kPairBK, T, 2 * long(T) * M);
+}
+
+// X scaled, the tokens' scales, and the splits' sums.
+static size_t gate_split_offset(int N, int T) { return up256(size_t(T) * N * 2) + up256(up16(T) * sizeof(float)); }
+size_t gemm_gated_workspace_bytes(int M, int N, int T) {
+  const int splits = gate_plan(M, N, T).splits;
+  return gate_split_offset(N, T) + (splits > 1 ? size_t(splits) * 2 * T * M * sizeof(float) : 0);
 }
 
 cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_gate, const Shape& gate,
@@ -646,7 +762,8 @@ cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_
   p.T = T;
   p.stages = gate.N / kPairBK;
   p.row_tiles = (gate.M + 127) / 128;
-  set_tokens(p, pair_token_tile(p.row_tiles, p.stages, T, pair_count<kGate>()));
+  set_plan(p, gate_plan(gate.M, gate.N, T));
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gate_split_offset(gate.N, T));
   p.idesc = tc_idesc_f16(256, p.n_acc, false, false, false);
   p.inverse = inverse;
   p.out = H;
@@ -682,11 +799,24 @@ cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_
 
 // ---- input gradient ----
 
+static PairPlan grad_plan(int nmat, const Shape* shapes, int T) {
+  int stages = 0;
+  for (int i = 0; i < nmat; ++i) stages += (shapes[i].M + kPairBK - 1) / kPairBK;
+  return pair_plan((shapes[0].N + 255) / 256, stages, T, long(T) * shapes[0].N);
+}
+
+// The splits' sums.
+size_t gemm_grad_x_workspace_bytes(int nmat, const Shape* shapes, int T) {
+  const int splits = grad_plan(nmat, shapes, T).splits;
+  return splits > 1 ? size_t(splits) * T * shapes[0].N * sizeof(float) : 0;
+}
+
 // dX from dY_s already scaled to fp16 (rows `ld[s]` apart, zeros beyond M_s)
-// with the tokens' inverse scales.
+// with the tokens' inverse scales; workspace as sized by
+// gemm_grad_x_workspace_bytes, 16-byte aligned.
 cudaError_t launch_gemm_grad_x(int nmat, const uint8_t* const* packed, const uint16_t* const* alpha,
                                const Shape* shapes, const uint16_t* const* dys, const int* ld, const float* inverse,
-                               int T, uint16_t* dX, cudaStream_t stream) {
+                               int T, uint16_t* dX, void* workspace, cudaStream_t stream) {
   PairMaps maps;
   PairParams p = {};
   p.nmat = nmat;
@@ -697,7 +827,8 @@ cudaError_t launch_gemm_grad_x(int nmat, const uint8_t* const* packed, const uin
     p.mat[i].stages = (shapes[i].M + kPairBK - 1) / kPairBK;
     p.stages += p.mat[i].stages;
   }
-  set_tokens(p, pair_token_tile(p.row_tiles, p.stages, T, pair_count<kGrad>()));
+  set_plan(p, grad_plan(nmat, shapes, T));
+  p.partial = static_cast<float*>(workspace);
   p.idesc = tc_idesc_f16(256, p.n_acc, false, true, false);
   p.inverse = inverse;
   p.out = dX;

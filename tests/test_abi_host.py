@@ -293,7 +293,7 @@ def test_finetune_binding_refuses_cpu_tensors(L):
 
 def test_gemm_gated_sizes_and_argument_errors(L):
     up = lambda n, m: (n + m - 1) // m * m
-    assert L.mbok_gemm_gated_workspace_bytes(100, 256, 33) == up(33 * 256 * 2, 256) + up(33, 16) * 4
+    assert L.mbok_gemm_gated_workspace_bytes(100, 256, 33) == up(33 * 256 * 2, 256) + up(up(33, 16) * 4, 256)
     assert L.mbok_gemm_gated_workspace_bytes(100, 250, 33) == 0 and L.mbok_gemm_gated_workspace_bytes(100, 256, 0) == 0
     g = lambda **kw: L.mbok_gemm_gated(*[kw.get(k, v) for k, v in dict(
         pg=FAKE, ag=FAKE, Kg=3, pu=FAKE, au=FAKE, Ku=2, M=64, N=1024, group=128, X=FAKE, T=40, H=FAKE, gate=None,
