@@ -7,18 +7,23 @@
 // product over a 128-column group is an exact MMA, scaled per group in fp32; the
 // rest is arranged for the instruction count, which bounds this size:
 //
-//  * Bits as they are.  A single set bit i < 10 of an fp16 word is the subnormal
-//    2^(i - 24), exact for the tensor cores.  Column i of a row's 16 is bit i of
+//  * Bits as they are.  A single set bit of an fp16 word is a power of two, exact
+//    for the tensor cores: bits 5 .. 9 are the subnormals 2^-19 .. 2^-15, bits 10,
+//    11 and 12 are 2^-14, 2^-13 and 2^-11.  Column i of a row's 16 is bit i of
 //    its halfword, so with bytes 0 and 1 in the two halves of a word (one byte
-//    permute) the fragment word of columns (i, i + 8) is one AND with 0x00010001
-//    << i.  The activations carry the inverse factor: 2^(7 - i) x S in fp16, S a
-//    power of two per warp and vector that puts the largest finite |x| below 2^8
-//    (exact for bf16 values down to 2^-24 of the largest, off by at most 2^-32 of
-//    it below).  With T the sum over set bits and X the sum over all columns (an
-//    MMA with every bit set, once per group), the +-1 sum is 2 T - X.  Building
-//    +-1 words took a logic and a multiply-add instruction each and more around
-//    them: 23 instructions per MMA, 35.8 us for two to eight vectors (LLaMA-7B gate
-//    and up, K = 3).
+//    permute), five bits up, the fragment word of columns (i, i + 8) is one AND
+//    with 0x00200020 << i.  The activations carry the inverse factor (2^8 .. 1)
+//    and S, a power of two per warp and vector that puts the largest finite |x|
+//    below 2^7 (exact for bf16 values down to 2^-23 of the largest, off by at most
+//    2^-31 of it below).  With T the sum over set bits and X the sum over all
+//    columns (an MMA with every bit set, once per group), the +-1 sum is 2 T - X.
+//    Building +-1 words took a logic and a multiply-add instruction each and more
+//    around them: 23 instructions per MMA, 35.8 us for two to eight vectors
+//    (LLaMA-7B gate and up, K = 3) against 27.1.
+//    The five bits up are for accuracy: products are aligned for their sum as if a
+//    subnormal had a leading one, so a subnormal's product is cut off 2^z too
+//    early, z its leading zeros.  With the bits left at 0 .. 7 (z up to 10) h was
+//    off by 1.8e-6 of its norm (fp32 activations 5e-6); at 5 .. 12 by 1.0e-7.
 //  * Persistent CTAs.  A warp owns at most two 128-column groups and keeps their
 //    activations in registers as MMA fragments for all rows it meets; it streams
 //    the bits and scales of its columns for one row octet after another through
@@ -46,6 +51,7 @@ cudaError_t launch_gemv_lut_gated(const uint8_t*, const uint16_t*, const Shape&,
                                   const Shape&, const void*, bool, void*, bool, void*, cudaStream_t, bool);
 size_t gemv_gated_lut_workspace_bytes(const Shape&);
 
+constexpr float kGdProduct = 2048.f;         // x S over the product of a set bit and its activation
 constexpr int kGdMaxDepth = 4;               // steps in flight per warp: as many as fit, at least 2
 constexpr int kGdSmemMax = 227 * 1024, kGdStatic = 1024;   // of which static (barriers)
 constexpr int kGdGroups = 2;                 // groups per warp
@@ -58,7 +64,7 @@ template <int NT>
 struct GdGeom {
   static constexpr int kMaxWarps = NT == 1 ? 20 : 16;
   static constexpr int kRed = 2 * 16 * 8 * NT + 2;          // floats per warp: [gate, up][row][column], padded
-  static constexpr int kConst = (kGdGroups + 1) * 8 * NT;   // floats per warp: X of each group, 2^17 / S
+  static constexpr int kConst = (kGdGroups + 1) * 8 * NT;   // floats per warp: X of each group, 1 / S
 };
 // Shared memory of one warp besides its ring: two buffers of sums and constants.
 template <int NT>
@@ -100,27 +106,27 @@ __device__ __forceinline__ void gd_mma0(float d[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// The fragment word of columns (I, I + 8) from a row's 16 bits as bytes 0 and 2.
+// The fragment word of columns (I, I + 8) from a row's 16 bits, 0..7 at bits 5..12
+// and 8..15 at bits 21..28.
 template <int I>
-__device__ __forceinline__ uint32_t gd_word(uint32_t u) { return u & (0x00010001u << I); }
+__device__ __forceinline__ uint32_t gd_word(uint32_t u) { return u & (0x00200020u << I); }
 
 // d (from zero where FIRST) += 64 columns of two planes' rows (their bits u0, u1)
 // times the fragments b.
 template <int NT, bool FIRST>
 __device__ __forceinline__ void gd_chunk(float d[NT][4], uint32_t u0, uint32_t u1, const uint32_t b[NT][8]) {
-#define MBOK_GD_STEP(J)                                                                                    \
-  _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) {                                                      \
-    if (FIRST && J == 0)                                                                                   \
-      gd_mma0(d[nt], gd_word<2 * J>(u0), gd_word<2 * J>(u1), gd_word<2 * J + 1>(u0), gd_word<2 * J + 1>(u1), \
-              b[nt][2 * J], b[nt][2 * J + 1]);                                                             \
-    else                                                                                                   \
-      gd_mma(d[nt], gd_word<2 * J>(u0), gd_word<2 * J>(u1), gd_word<2 * J + 1>(u0), gd_word<2 * J + 1>(u1), \
-             b[nt][2 * J], b[nt][2 * J + 1]);                                                              \
+#define MBOK_GD_STEP(J, MMA)                                                                                \
+  _Pragma("unroll") for (int nt = 0; nt < NT; ++nt)                                                         \
+      MMA(d[nt], gd_word<2 * J>(u0), gd_word<2 * J>(u1), gd_word<2 * J + 1>(u0), gd_word<2 * J + 1>(u1),    \
+          b[nt][2 * J], b[nt][2 * J + 1]);
+  if (FIRST) {
+    MBOK_GD_STEP(0, gd_mma0)
+  } else {
+    MBOK_GD_STEP(0, gd_mma)
   }
-  MBOK_GD_STEP(0)
-  MBOK_GD_STEP(1)
-  MBOK_GD_STEP(2)
-  MBOK_GD_STEP(3)
+  MBOK_GD_STEP(1, gd_mma)
+  MBOK_GD_STEP(2, gd_mma)
+  MBOK_GD_STEP(3, gd_mma)
 #undef MBOK_GD_STEP
 }
 
@@ -167,11 +173,11 @@ struct GdUnit {
     }
     return m;
   }
-  // Fragments: column i (and i + 8) times scale times 2^(7 - i).
+  // Fragments: column i (and i + 8) times scale over (kGdProduct times bit 5 + i).
   __device__ __forceinline__ void fragment(float scale, int part, uint32_t b[8]) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float f = float(1 << (7 - i));
+      const float f = i < 7 ? float(1 << (8 - i)) : 1.f;
       float lo, hi;
       if (XF32) {
         lo = gd_part(at(i) * scale, part) * f;
@@ -315,25 +321,27 @@ gemv_gated_kernel(const __grid_constant__ GatedMmaParams p) {
       }
     high = max(high, __shfl_xor_sync(0xffffffffu, high, 1));
     high = max(high, __shfl_xor_sync(0xffffffffu, high, 2));
-    // S = 2^e, e = 7 - floor(log2 high): at most 2^126 (tiny vectors), 1 for zeros
-    const int e = high == 0u ? 0 : min(134 - int(high >> 23), 126);
+    // S = 2^e, e = 6 - floor(log2 high): at most 2^126 (tiny vectors), 1 for zeros
+    const int e = high == 0u ? 0 : min(133 - int(high >> 23), 126);
     const float scale = __uint_as_float(uint32_t(127 + e) << 23);
 #pragma unroll
     for (int g = 0; g < kGdGroups; ++g)
 #pragma unroll
       for (int c = 0; c < 2; ++c) x[g][c].fragment(scale, n % 3, b[g][c][nt]);
-    // 2^17 / S of the column; accumulator columns are 2t and 2t + 1
-    if (t == 0) consts[(kGdGroups * NT + nt) * 8 + gq] = __uint_as_float(uint32_t(127 - e) << 23) * 131072.f;
+    // 1 / S of the column; accumulator columns are 2t and 2t + 1
+    if (t == 0) consts[(kGdGroups * NT + nt) * 8 + gq] = __uint_as_float(uint32_t(127 - e) << 23);
   }
   // X of each group and column: every bit set (row 0 of the product)
 #pragma unroll
   for (int g = 0; g < kGdGroups; ++g) {
     float d[NT][4];
-    gd_chunk<NT, true>(d, 0x00FF00FFu, 0u, b[g][0]);
-    gd_chunk<NT, false>(d, 0x00FF00FFu, 0u, b[g][1]);
+    gd_chunk<NT, true>(d, 0x1FE01FE0u, 0u, b[g][0]);
+    gd_chunk<NT, false>(d, 0x1FE01FE0u, 0u, b[g][1]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      if (gq == 0) *reinterpret_cast<float2*>(consts + (g * NT + nt) * 8 + 2 * t) = make_float2(d[nt][0], d[nt][1]);
+      if (gq == 0)
+        *reinterpret_cast<float2*>(consts + (g * NT + nt) * 8 + 2 * t) =
+            make_float2(d[nt][0] * kGdProduct, d[nt][1] * kGdProduct);
   }
   __syncwarp();
   if (!p.weights_static) {
@@ -374,7 +382,7 @@ gemv_gated_kernel(const __grid_constant__ GatedMmaParams p) {
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int oi = 0; oi < 2; ++oi)
-              u[c][oi] = __byte_perm(*reinterpret_cast<const uint16_t*>(bits + oi * kGdUnits * 16 + 64 * c), 0u, 0x4140);
+              u[c][oi] = __byte_perm(*reinterpret_cast<const uint16_t*>(bits + oi * kGdUnits * 16 + 64 * c), 0u, 0x4140) * 32u;
           gd_chunk<NT, true>(d, u[0][0], u[0][1], b[g][0]);
           gd_chunk<NT, false>(d, u[1][0], u[1][1], b[g][1]);
           // the +-1 sums 2 T - X times the plane's group scales
@@ -385,8 +393,8 @@ gemv_gated_kernel(const __grid_constant__ GatedMmaParams p) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float2 X = *reinterpret_cast<const float2*>(consts + (g * NT + nt) * 8 + 2 * t);
-              y[m][nt][2 * oi] = fmaf(a, fmaf(2.f, d[nt][2 * oi], -X.x), y[m][nt][2 * oi]);
-              y[m][nt][2 * oi + 1] = fmaf(a, fmaf(2.f, d[nt][2 * oi + 1], -X.y), y[m][nt][2 * oi + 1]);
+              y[m][nt][2 * oi] = fmaf(a, fmaf(2.f * kGdProduct, d[nt][2 * oi], -X.x), y[m][nt][2 * oi]);
+              y[m][nt][2 * oi + 1] = fmaf(a, fmaf(2.f * kGdProduct, d[nt][2 * oi + 1], -X.y), y[m][nt][2 * oi + 1]);
             }
           }
         }

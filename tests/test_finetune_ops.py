@@ -172,6 +172,37 @@ def test_gemv_gated_extremes():
             assert torch.isnan(h[1]).all()
 
 
+def test_gemv_gated_fp32_accuracy():
+    # In norm, where errors do not line up as in the bound above: a group's sum is
+    # eight MMAs, each cutting off at most 2^-23 of a running sum whose root mean
+    # square is at most the group's own, so g and u are off by at most 2^-20 of
+    # their norm (the groups' errors add as their sums do), and h, with |silu'| <
+    # 1.1 and g u ~ h, by twice that; observed errors are a tenth of it.
+    for kg, ku, M, N, batch, x_dtype in ((3, 2, 599, 768, 8, "bf16"), (1, 1, 300, 4096, 4, "f32"),
+                                         (2, 4, 400, 128, 16, "f32"), (3, 3, 200, 5248, 16, "bf16")):
+        gate, up = Layer(kg, M, N, 41), Layer(ku, M, N, 42)
+        x, x64 = _x(batch, N, 43, x_dtype)
+        h = _gemv_gated(gate, up, x_dev(x, x_dtype), x_dtype, batch, "f32")
+        g, _ = F.project(gate.words, gate.alpha, kg, M, N, x64)
+        u, _ = F.project(up.words, up.alpha, ku, M, N, x64)
+        want = F.silu(g) * u
+        assert np.linalg.norm(_f64(h) - want) <= 2.0 ** -19 * np.linalg.norm(want)
+
+
+def test_gemv_gated_huge_activations():
+    # activations near the type's highest: a closed gate gives 0, not infinity x 0
+    import torch
+    M, N, batch = 24, 256, 3
+    gate, up = Layer(1, M, N, 51), Layer(1, M, N, 52)
+    gate.blocked.zero_()
+    up.blocked.fill_(2.0 ** -14)   # |u| <= 256 x 2^126 x 2^-14
+    for x_dtype in ("bf16", "f32"):
+        x = torch.full((batch, N), 2.0 ** 126, dtype=_dt(x_dtype), device="cuda")
+        x[:, ::3] *= -1
+        h = _gemv_gated(gate, up, x, x_dtype, batch, "f32")
+        assert torch.equal(h, torch.zeros_like(h))
+
+
 def test_gemv_gated_deterministic_and_graph():
     import torch
     import boolean_weight_matmul_b200 as mb
