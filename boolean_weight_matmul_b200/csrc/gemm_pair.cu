@@ -40,8 +40,10 @@
 // stage to both CTAs' `empty` barriers.  Four epilogue warps, one per
 // tensor-memory lane quarter, drain finished tiles; the unpack warps join them
 // for a CTA's last tile and for every two-accumulator tile.
-// With few tiles the contraction is split over several pairs, which leave fp32
-// sums in the workspace; a second kernel adds them in order (and gates).
+// Tiles that fill the last wave badly are dealt out as one run of stages, cut into
+// equal parts wherever that falls: a pair may begin and end inside a tile, leaves
+// such a tile's fp32 sums in the workspace, and a second kernel adds them in order
+// (and gates).
 // Every mbarrier wait is bounded (1 s): on timeout the CTA records an error
 // flag, drains what it issued (bounded) and leaves with the other.
 #include "scale_rows.h"
@@ -72,6 +74,7 @@ constexpr int kPairUnpackWarp0 = 3;                           // after the two c
 constexpr int kPairEpiWarp0 = kPairUnpackWarp0 + kPairUnpackWarps;
 constexpr int kPairThreads = (kPairEpiWarp0 + 4) * 32;
 constexpr unsigned kPairTmemCols = 512;                       // accumulators at columns 0 and 256
+constexpr int kPairSums = 2 * kPairRows;                      // sums per token and tile: GATE 128 rows of gate, of up
 
 static __device__ unsigned int g_pair_error;
 
@@ -101,27 +104,57 @@ struct PairParams {
   int stages;          // per tile
   int row_tiles;       // tiles along W's rows (GATE, 128) or columns (GRAD, 256)
   int ntiles;
-  int splits, nitems;  // parts of the contraction; tiles x splits
+  int workers;         // 0: pairs take whole tiles in turn; else the stages of all tiles are cut into this many runs,
+  int run, run_rest;   // of `run` + run_rest / workers stages
   uint32_t idesc;
   PairMul mul;
   const float* inverse;   // [T rounded up to 16]
   uint16_t* out;          // H, or dX
   uint16_t* gate;         // GATE: [T][M] or nullptr
   uint16_t* up;
-  float* partial;         // several splits: GRAD [split][T][N], GATE [split][gate, up][T][M]
+  float* partial;         // sums of tiles that a run begins or ends in: [run][first, last][n tokens][kPairSums]
 };
 
-// Item i of a launch: a tile and its part of the contraction (splits vary
-// slowest, then token tiles: pairs that run together share their tokens).
-struct PairItem {
-  int tile, split, k0, k1;
+// First stage of run w: w / workers of the stages of all tiles, rounded down.
+__device__ __forceinline__ int run_begin(const PairParams& p, int w) {
+  return w * p.run + int(unsigned(w * p.run_rest) / unsigned(p.workers));
+}
+
+// A pair's items: tiles tile0, tile0 + step, ..., the first from stage k_first,
+// the last up to k_last.  (Whole tiles: row tiles vary fastest, so that pairs that
+// run together share their tokens.)
+struct PairWalk {
+  int n, tile0, step, k_first, k_last;
 };
-__device__ __forceinline__ PairItem pair_item(const PairParams& p, int i) {
+struct PairItem {
+  int tile, k0, k1;
+  int slot;   // of `partial`, or -1: a whole tile
+};
+__device__ __forceinline__ PairWalk pair_walk(const PairParams& p, int pair, int npairs) {
+  PairWalk w;
+  if (p.workers == 0) {
+    w.n = (p.ntiles - 1 - pair) / npairs + 1;   // at least one
+    w.tile0 = pair;
+    w.step = npairs;
+    w.k_first = 0;
+    w.k_last = p.stages;
+  } else {
+    const int b = run_begin(p, pair), e = run_begin(p, pair + 1);
+    w.tile0 = b / p.stages;
+    const int last = (e - 1) / p.stages;
+    w.n = last - w.tile0 + 1;
+    w.step = 1;
+    w.k_first = b - w.tile0 * p.stages;
+    w.k_last = e - last * p.stages;
+  }
+  return w;
+}
+__device__ __forceinline__ PairItem pair_item(const PairParams& p, const PairWalk& w, int pair, int i) {
   PairItem it;
-  it.split = i / p.ntiles;
-  it.tile = i - it.split * p.ntiles;
-  it.k0 = int(long(it.split) * p.stages / p.splits);
-  it.k1 = int(long(it.split + 1) * p.stages / p.splits);
+  it.tile = w.tile0 + i * w.step;
+  it.k0 = i == 0 ? w.k_first : 0;
+  it.k1 = i + 1 == w.n ? w.k_last : p.stages;
+  it.slot = it.k1 - it.k0 == p.stages ? -1 : 2 * pair + (i > 0 ? 1 : 0);
   return it;
 }
 
@@ -306,14 +339,11 @@ __device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, c
       v[4 * i + 2] = __uint_as_float(w[4 * i + 2]) * s.z;
       v[4 * i + 3] = __uint_as_float(w[4 * i + 3]) * s.w;
     }
-    if (p.splits > 1) {
-      if (r < rows) {
-        const size_t plane = MODE == kGate ? size_t(2 * it.split + (lane >> 4)) : size_t(it.split);
-        float* at = p.partial + (plane * p.T + t) * rows + r;
+    if (it.slot >= 0) {
+      float* at = p.partial + (size_t(it.slot) * p.n + 16 * j) * kPairSums +
+                  (MODE == kGate ? 128 * (lane >> 4) + rank * 64 + 16 * q + (lane & 15) : rank * 128 + 32 * q + lane);
 #pragma unroll
-        for (int i = 0; i < 16; ++i, at += rows)
-          if (t + i < p.T) __stcg(at, v[i]);
-      }
+      for (int i = 0; i < 16; ++i) __stcg(at + i * kPairSums, v[i]);
     } else if (MODE == kGrad) {
       store_rows<16>(pairs, p.out, rows, rows, p.T, r, t, v, lane);
     } else {
@@ -354,7 +384,8 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(pair_rank());
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int n_mine = (p.nitems - 1 - pair) / npairs + 1;   // items pair, pair + npairs, ...; at least one
+  const PairWalk walk = pair_walk(p, pair, npairs);
+  const int n_mine = walk.n;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairMaxSlots; ++s) {
@@ -392,7 +423,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     int s = 0, g = 0;
     unsigned ph = 1;   // parity of the slot's previous use
     for (int i = 0; i < n_mine && ok; ++i) {
-      const PairItem it = pair_item(p, pair + i * npairs);
+      const PairItem it = pair_item(p, walk, pair, i);
       const int t0 = (it.tile / p.row_tiles) * p.n + rank * (p.n_acc / 2);
       int m = 0, step = it.k0;   // GRAD: matrix and its 64-row step
       if (MODE == kGrad)
@@ -418,7 +449,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     int s = 0, g = 0;
     unsigned ph = 1;
     for (int i = 0; i < n_mine && ok; ++i) {
-      const PairItem it = pair_item(p, pair + i * npairs);
+      const PairItem it = pair_item(p, walk, pair, i);
       const int rt = it.tile % p.row_tiles;
       int m = 0, step = it.k0;
       if (MODE == kGrad)
@@ -466,7 +497,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         if (use > 0 && !pair_wait(&tempty[b], unsigned(use - 1) & 1u)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(b * 256);
-        const PairItem it = pair_item(p, pair + i * npairs);
+        const PairItem it = pair_item(p, walk, pair, i);
         for (int kb = it.k0; kb < it.k1; ++kb) {
           if (!pair_wait(&ready[s], ph)) { ok = false; break; }
           tc_fence_after();
@@ -497,7 +528,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     int s = grp, ws = grp, g = grp, first = grp;   // both rings have at least kPairGroups slots
     unsigned ph = 0, wph = 0;
     for (int i = 0; i < n_mine && ok; ++i) {
-      const PairItem it = pair_item(p, pair + i * npairs);
+      const PairItem it = pair_item(p, walk, pair, i);
       int m = 0, kb = it.k0 + first, step = kb;
       for (; kb < it.k1; kb += kPairGroups, step += kPairGroups, g += kPairGroups) {
         const unsigned char* w = wring + ws * kPairWBytes;
@@ -555,7 +586,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       if (!pair_wait(&tfull[b], unsigned(use) & 1u)) { ok = false; break; }
       tc_fence_after();
       const bool shared = p.naccs > 1 || i + 1 == n_mine;   // with the unpack warps: every fifth chunk
-      pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair_item(p, pair + i * npairs), rank, warp & 3, lane, 0,
+      pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair_item(p, walk, pair, i), rank, warp & 3, lane, 0,
                        shared ? 1 + kPairUnpackWarps / 4 : 1);
       tc_fence_before();
       __syncwarp();
@@ -580,51 +611,62 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   }
 }
 
-// dX, or H (and G and U), from the splits' sums in order; n = T x rows, 4 values
-// per thread where n allows.
+// dX, or H (and G and U), of the tiles that runs share: block y is the cut at the
+// start of run y + 1, and takes the tile that this is the first cut of.  A thread
+// adds 4 rows of one token, in the order of the runs.
 template <PairMode MODE>
-__global__ void __launch_bounds__(256) pair_join_kernel(const float* part, int splits, size_t n, uint16_t* out,
-                                                        uint16_t* gate, uint16_t* up) {
+__global__ void __launch_bounds__(256) pair_join_kernel(const __grid_constant__ PairParams p) {
   pdl_launch();
   pdl_wait();
-  const size_t i0 = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i0 >= n) return;
-  const bool vec = n % 4 == 0;   // every plane 16-byte aligned
-  constexpr int kPlanes = MODE == kGate ? 2 : 1;
+  const int w0 = blockIdx.y, cut = run_begin(p, w0 + 1);
+  const int tile = cut / p.stages, begin = tile * p.stages, end = begin + p.stages;
+  const int b0 = run_begin(p, w0);
+  if (cut == begin || b0 > begin) return;
+  int w1 = w0 + 1;   // the tile's last run
+  while (run_begin(p, w1 + 1) < end) ++w1;
+  constexpr int kRows = MODE == kGate ? kPairSums / 2 : kPairSums;   // of the tile
+  constexpr int kPlanes = kPairSums / kRows;
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  const int tok = i / (kRows / 4), row = i % (kRows / 4) * 4;
+  const int t = tile / p.row_tiles * p.n + tok, r = tile % p.row_tiles * kRows + row;
+  const int rows = MODE == kGate ? p.M : p.N;
+  if (tok >= p.n || t >= p.T || r >= rows) return;
   float sum[kPlanes][4] = {};
-  for (int s = 0; s < splits; ++s)
+  const size_t slot = size_t(p.n) * kPairSums, at = size_t(tok) * kPairSums + row;
+  // run w0 ends in this tile (its first tile or a later one), the others begin in it
+  const float* first = p.partial + (2 * w0 + (b0 < begin ? 1 : 0)) * slot + at;
+  const float* other = p.partial + 2 * w0 * slot + at;
+#pragma unroll 4
+  for (int w = 0; w <= w1 - w0; ++w) {
+    const float* src = w == 0 ? first : other + 2 * w * slot;
 #pragma unroll
     for (int m = 0; m < kPlanes; ++m) {
-      const float* at = part + (size_t(s) * kPlanes + m) * n + i0;
-      if (vec) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(at));
-        sum[m][0] += v.x; sum[m][1] += v.y; sum[m][2] += v.z; sum[m][3] += v.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i0 + e < n) sum[m][e] += __ldcg(at + e);
-      }
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + m * kRows));
+      sum[m][0] += v.x; sum[m][1] += v.y; sum[m][2] += v.z; sum[m][3] += v.w;
     }
+  }
+  const bool vec = rows % 4 == 0;   // 8-byte aligned, and all four rows there
   auto store = [&](uint16_t* to, const float* v) {
+    to += size_t(t) * rows + r;
     if (vec) {
-      *reinterpret_cast<uint2*>(to + i0) = make_uint2(tc_pack_bf16x2(v[0], v[1]), tc_pack_bf16x2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(to) = make_uint2(tc_pack_bf16x2(v[0], v[1]), tc_pack_bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (i0 + e < n) to[i0 + e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
+        if (r + e < rows) to[e] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
     }
   };
   if (MODE == kGrad) {
-    store(out, sum[0]);
+    store(p.out, sum[0]);
   } else {
-    if (gate != nullptr) {
-      store(gate, sum[0]);
-      store(up, sum[kPlanes - 1]);
+    if (p.gate != nullptr) {
+      store(p.gate, sum[0]);
+      store(p.up, sum[kPlanes - 1]);
     }
     float h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = gated_fast(sum[0][e], sum[kPlanes - 1][e]);
-    store(out, h);
+    store(p.out, h);
   }
 }
 
@@ -664,45 +706,56 @@ static int pair_count() {
   });
 }
 
-// Tokens per tile and splits of the contraction.
+// Tokens per tile, and runs of stages (0: whole tiles).
 struct PairPlan {
-  int n, splits;
+  int n, workers;
 };
 
-// Tiles of n tokens (a multiple of 32, at most 512) and splits that minimise the
-// time of the wave-quantised grid of kPlanPairs pairs (the plan does not ask the
-// device, so that a workspace's size does not depend on it).  In units of one
-// token's MMAs of a stage (about 1.1 ns): a stage costs its tokens, and at least
-// the unpack of its weights (320 tokens' worth); an item adds its pipeline's fill
-// and what of its drain is not hidden (4 stages, 12 with two accumulators);
-// splits add their sums' way through memory (at 5 TB/s) and a launch (2 us).
-// Measured: dX of 9998 x 896, K = 2, 32 tokens 66.8 us unsplit; gated 389 rows,
-// N = 3456, 1027 tokens 32.6 us.
+// The tile width (a multiple of 32, at most 512) and the cut that minimise the
+// time of kPlanPairs pairs (the plan does not ask the device, so that a
+// workspace's size does not depend on it).  In units of one token's MMAs of a
+// stage (about 1.1 ns): a stage costs its tokens, and at least the unpack of its
+// weights (320 tokens' worth); a launch adds its pipeline's fill (4 stages), an
+// item what of its drain is not hidden (1 stage, 12 with two accumulators); runs
+// add their sums' way through memory (at 4 TB/s) and a launch (4 us).  Runs that
+// cut every tile alike leave one part each, others up to two.  Uncut and cut: dX
+// of 9998 x 896, K = 2, 32 tokens 67 and 25 us; gate and up of LLaMA-7B, 32 tokens
+// 73 and 52 us, their dX for 256 tokens 185 and 67 us.
 constexpr int kPlanPairs = 74;
-constexpr int kPairMaxSplits = 16;
-static PairPlan pair_plan(int row_tiles, int stages, int T, long out_floats) {
-  PairPlan best = {512, 1};
+constexpr int kPairMinRun = 4;   // stages
+static PairPlan pair_plan(int row_tiles, int stages, int T) {
+  PairPlan best = {512, 0};
   double best_cost = -1;
   const int most = T >= 512 ? 512 : (T + 31) / 32 * 32;
   static const int kWidths[] = {512, 448, 416, 384, 352, 320, 288, 256, 224, 192, 160, 128, 96, 64, 32};
-  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, kPairMaxSplits};
   for (const int n : kWidths) {
     if (n > most) continue;
     const long tiles = long(row_tiles) * ((T + n - 1) / n);
-    for (const int s : kSplits) {
-      if (s > 1 && (s * 4 > stages + 3 || tiles * s > 8 * kPlanPairs)) break;   // short parts, or the grid is full
-      const double waves = double((tiles * s + kPlanPairs - 1) / kPlanPairs);
-      const double per_item = double((stages + s - 1) / s) + (n > 256 ? 12 : 4);
-      double cost = waves * (n > 320 ? n : 320) * per_item;
-      if (s > 1) cost += (8.0 * s * double(out_floats) / 5000.0 + 2000.0) / 1.1;
-      if (best_cost < 0 || cost < best_cost) {
-        best_cost = cost;
-        best.n = n;
-        best.splits = s;
-      }
-    }
+    const double stage = n > 320 ? n : 320, drain = n > 256 ? 12 : 1;
+    auto consider = [&](double cost, int workers) {
+      if (best_cost >= 0 && cost >= best_cost) return;
+      best_cost = cost;
+      best.n = n;
+      best.workers = workers;
+    };
+    consider(stage * (double((tiles + kPlanPairs - 1) / kPlanPairs) * (stages + drain) + 4), 0);
+    if (tiles > 8 * kPlanPairs) continue;
+    auto cut = [&](int workers) {
+      const double run = double(tiles) * stages / workers;
+      if (workers < 2 || run < kPairMinRun) return;
+      const double parts = workers % tiles == 0 ? workers : (workers < tiles ? 2.0 * workers : double(workers + tiles));
+      const double items = workers % tiles == 0 ? 1 : 2 + double(int(run / stages));
+      consider(stage * (run + items * drain + 4) + (parts * n * kPairSums * 8 / 4000.0 + 4000.0) / 1.1, workers);
+    };
+    for (int k = 2; k * tiles < kPlanPairs; ++k) cut(int(k * tiles));
+    cut(kPlanPairs);
   }
   return best;
+}
+
+// Sums of the runs' first and last tiles.
+static size_t plan_workspace_bytes(const PairPlan& pl) {
+  return size_t(2) * pl.workers * pl.n * kPairSums * sizeof(float);
 }
 
 template <PairMode MODE>
@@ -715,13 +768,19 @@ static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t
   p.wslots = wslots < kPairMaxSlots ? wslots : kPairMaxSlots;
   for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
   const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
-  const int grid = 2 * (p.nitems < pairs ? p.nitems : pairs);
+  if (p.workers > pairs) p.workers = pairs;   // longer runs, whose sums take no more room
+  if (p.workers > 0) {
+    p.run = p.ntiles * p.stages / p.workers;
+    p.run_rest = p.ntiles * p.stages % p.workers;
+  }
+  const int items = p.workers > 0 ? p.workers : p.ntiles;
+  const int grid = 2 * (items < pairs ? items : pairs);
   const cudaError_t e =
       launch_dependent(gemm_pair_kernel<MODE>, dim3(grid), dim3(kPairThreads), size_t(smem), stream, maps, p);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const size_t n = size_t(p.T) * (MODE == kGate ? p.M : p.N);
-  return launch_dependent(pair_join_kernel<MODE>, dim3(unsigned((n + 1023) / 1024)), dim3(256), 0, stream,
-                          static_cast<const float*>(p.partial), p.splits, n, p.out, p.gate, p.up);
+  if (e != cudaSuccess || p.workers < 2) return e;
+  constexpr int kThreadsPerToken = (MODE == kGate ? kPairSums / 2 : kPairSums) / 4;
+  return launch_dependent(pair_join_kernel<MODE>, dim3(unsigned((p.n * kThreadsPerToken + 255) / 256), p.workers - 1),
+                          dim3(256), 0, stream, p);
 }
 
 static void set_plan(PairParams& p, const PairPlan& pl) {
@@ -729,8 +788,7 @@ static void set_plan(PairParams& p, const PairPlan& pl) {
   p.naccs = p.n > 256 ? 2 : 1;
   p.n_acc = p.n / p.naccs;   // n is a multiple of 32
   p.ntiles = p.row_tiles * ((p.T + p.n - 1) / p.n);
-  p.splits = pl.splits;
-  p.nitems = p.ntiles * p.splits;
+  p.workers = pl.workers;
 }
 
 static size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -739,14 +797,13 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // ---- gated forward ----
 
 static PairPlan gate_plan(int M, int N, int T) {
-  return pair_plan((M + 127) / 128, N / kPairBK, T, 2 * long(T) * M);
+  return pair_plan((M + 127) / 128, N / kPairBK, T);
 }
 
-// X scaled, the tokens' scales, and the splits' sums.
-static size_t gate_split_offset(int N, int T) { return up256(size_t(T) * N * 2) + up256(up16(T) * sizeof(float)); }
+// X scaled, the tokens' scales, and the runs' sums.
+static size_t gate_sums_offset(int N, int T) { return up256(size_t(T) * N * 2) + up256(up16(T) * sizeof(float)); }
 size_t gemm_gated_workspace_bytes(int M, int N, int T) {
-  const int splits = gate_plan(M, N, T).splits;
-  return gate_split_offset(N, T) + (splits > 1 ? size_t(splits) * 2 * T * M * sizeof(float) : 0);
+  return gate_sums_offset(N, T) + plan_workspace_bytes(gate_plan(M, N, T));
 }
 
 cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_gate, const Shape& gate,
@@ -763,7 +820,7 @@ cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_
   p.stages = gate.N / kPairBK;
   p.row_tiles = (gate.M + 127) / 128;
   set_plan(p, gate_plan(gate.M, gate.N, T));
-  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gate_split_offset(gate.N, T));
+  p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gate_sums_offset(gate.N, T));
   p.idesc = tc_idesc_f16(256, p.n_acc, false, false, false);
   p.inverse = inverse;
   p.out = H;
@@ -802,13 +859,12 @@ cudaError_t launch_gemm_gated(const uint8_t* packed_gate, const uint16_t* alpha_
 static PairPlan grad_plan(int nmat, const Shape* shapes, int T) {
   int stages = 0;
   for (int i = 0; i < nmat; ++i) stages += (shapes[i].M + kPairBK - 1) / kPairBK;
-  return pair_plan((shapes[0].N + 255) / 256, stages, T, long(T) * shapes[0].N);
+  return pair_plan((shapes[0].N + 255) / 256, stages, T);
 }
 
-// The splits' sums.
+// The runs' sums.
 size_t gemm_grad_x_workspace_bytes(int nmat, const Shape* shapes, int T) {
-  const int splits = grad_plan(nmat, shapes, T).splits;
-  return splits > 1 ? size_t(splits) * T * shapes[0].N * sizeof(float) : 0;
+  return plan_workspace_bytes(grad_plan(nmat, shapes, T));
 }
 
 // dX from dY_s already scaled to fp16 (rows `ld[s]` apart, zeros beyond M_s)

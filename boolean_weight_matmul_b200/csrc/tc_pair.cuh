@@ -43,20 +43,23 @@ __device__ __forceinline__ void pair_tma_load_2d(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// As tc_wait, ordered after arrivals from either CTA.
+// As tc_wait, ordered after arrivals from either CTA.  A try may suspend the warp
+// for up to 20 us: many warps wait long, and their polling took issue slots from
+// the unpack (32 tokens, 11008 x 2 x 4096: 51 -> 49 us).
+constexpr unsigned kPairTryNs = 20000;
 __device__ __forceinline__ bool pair_wait(uint64_t* bar, unsigned parity, unsigned long long limit = kTcWaitNs) {
   const uint32_t a = tc_smem(bar);
   unsigned long long t0 = 0;
   for (unsigned it = 1;; ++it) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
-        : "r"(a), "r"(parity)
+        : "r"(a), "r"(parity), "r"(kPairTryNs)
         : "memory");
     if (done) return true;
-    if ((it & 255u) == 0) {
+    if ((it & 7u) == 0) {
       const unsigned long long t = tc_ns();
       if (t0 == 0) t0 = t;
       else if (t - t0 > limit) return false;
