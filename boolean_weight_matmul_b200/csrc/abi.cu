@@ -111,6 +111,12 @@ namespace {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two buffers share memory (NULL shares none).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 // Common shape checks; returns MBOK_OK or the first failing status.
@@ -342,6 +348,8 @@ int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int
   const size_t need = gemv_gated_workspace_bytes(gate, batch);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16)))
     return MBOK_ERR_WORKSPACE;
+  if (overlap(h, size_t(batch) * M * dtype_bytes(h_dtype), x, size_t(batch) * N * dtype_bytes(x_dtype)))
+    return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_gemv_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate, gate,
                                      reinterpret_cast<const uint8_t*>(packed_up), alpha_up, up, x,
                                      x_dtype == MBOK_F32, batch, h, h_dtype == MBOK_BF16, workspace,
@@ -358,6 +366,11 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
   if (!aligned(dH, 16) || !aligned(gate, 16) || !aligned(up, 16) || !aligned(dgate, 16) || !aligned(dup, 16) ||
       !aligned(H, 16))
     return MBOK_ERR_ALIGN;
+  if (overlap(dgate, n * 2, dup, n * 2) || overlap(dgate, n * 2, H, n * 2) || overlap(dup, n * 2, H, n * 2))
+    return MBOK_ERR_INVALID_ARG;
+  for (const uint16_t* out : {dgate, dup, H})
+    for (const uint16_t* in : {dH, gate, up})
+      if (out != in && overlap(out, n * 2, in, n * 2)) return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_gated_backward(dH, gate, up, n, dgate, dup, H, as_stream(stream)));
 }
 
@@ -382,6 +395,9 @@ int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int
     return MBOK_ERR_ALIGN;
   if (workspace == nullptr || workspace_bytes < gemm_gated_workspace_bytes(M, N, T) || !aligned(workspace, 256))
     return MBOK_ERR_WORKSPACE;
+  const size_t bytes = size_t(T) * M * 2;
+  if (overlap(H, bytes, gate, bytes) || overlap(H, bytes, up, bytes) || overlap(gate, bytes, up, bytes))
+    return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_gemm_gated(reinterpret_cast<const uint8_t*>(packed_gate), alpha_gate,
                                      make_shape(K_gate, M, N), reinterpret_cast<const uint8_t*>(packed_up), alpha_up,
                                      make_shape(K_up, M, N), X, T, H, gate, up, workspace, as_stream(stream)));
@@ -423,6 +439,11 @@ int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* 
   if (workspace == nullptr || workspace_bytes < gemm_backward_workspace_bytes(nseg, shapes, T) ||
       !aligned(workspace, 256))
     return MBOK_ERR_WORKSPACE;
+  // the scales' gradients read X and dY while dX is written
+  const size_t x_bytes = size_t(T) * N * 2;
+  if (any && overlap(dX, x_bytes, X, x_bytes)) return MBOK_ERR_INVALID_ARG;
+  for (int i = 0; i < nseg; ++i)
+    if (any && overlap(dX, x_bytes, dY[i], size_t(T) * M[i] * 2)) return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_gemm_backward(nseg, p8, alpha, shapes, X, T, dY, dX, dalpha, workspace, as_stream(stream)));
 }
 

@@ -284,27 +284,34 @@ size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int b
  *             value rounded once), aligned to its element, fully overwritten.
  *   Other arguments as mbok_gemv (workspace sized by
  *   mbok_gemv_gated_workspace_bytes; mbok_gemv_set_static_weights applies).
+ *   h must not overlap x (MBOK_ERR_INVALID_ARG).
  * One vector runs on the lookup kernel (one launch over both matrices and the
  * small launch that adds the slabs' partials and gates), two to 16 on the
  * tensor cores (one launch per 16 bf16 or 5 fp32 vectors, and for wide N a
  * small one that adds column slabs).
- * g and u have the accuracy of mbok_gemv; deterministic. */
+ * g and u have the accuracy of mbok_gemv, with two vectors or more an absolute
+ * error of 2^-31 of the vector's largest |x| per term besides; deterministic.
+ * An infinite activation makes its vector's h NaN with two vectors or more.
+ * Bounded waits: bit 2 of mbok_read_device_errors. */
 int mbok_gemv_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
                     const uint16_t* alpha_up, int K_up, int M, int N, int group, const void* x, int x_dtype, int batch,
                     void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace mbok_gemm_gated needs (256-byte aligned, no
  * initialisation; calls that share one must not run concurrently): X scaled
- * to fp16 and the tokens' scales.  0 on a bad argument. */
+ * to fp16, the tokens' scales and, where tiles are cut, their parts' fp32 sums.
+ * 0 on a bad argument. */
 size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T);
 
 /* The gated feed-forward block's first half for T tokens (prompts, training):
  *     H[t][r] = silu(G) * U,   G[t][r] = sum_j W_gate[r][j] X[t][j],
  *     U[t][r] = sum_j W_up[r][j] X[t][j],
- * on the tensor cores, both projections and the gate in one kernel.
+ * on the tensor cores, both projections and the gate in one kernel (few tiles are
+ * cut along N, and a second small kernel adds the parts and gates).
  *   X        : bf16 [T][N].   H: out, bf16 [T][M].
  *   gate, up : out, bf16 [T][M]: G and U for mbok_gated_backward, or both NULL.
- *   All 16-byte aligned; 1 <= T <= 2^23.  Other arguments as mbok_gemv_gated.
+ *   All 16-byte aligned; 1 <= T <= 2^23.  H, gate and up must not overlap one
+ *   another (MBOK_ERR_INVALID_ARG).  Other arguments as mbok_gemv_gated.
  *   workspace: mbok_gemm_gated_workspace_bytes(M, N, T) bytes.
  * Each token's X is scaled by a power of two into fp16 (exact, but for values
  * below 2^-29 of the token's largest, which are off by at most 2^-40 of it),
@@ -332,11 +339,13 @@ size_t mbok_gemm_backward_workspace_bytes(int nseg, const int* K, const int* M, 
  *   dalpha : host array of device pointers, out, fp32 in the layout of alpha
  *            (mbok_alpha_elems(K[s], M[s], N) elements, pad rows 0), or NULL;
  *            an entry may be NULL (a matrix whose scales are frozen).
- *   All 16-byte aligned; 1 <= T <= 2^23.
+ *   All 16-byte aligned; 1 <= T <= 2^23.  With dalpha asked for, dX must not
+ *   overlap X or a dY (MBOK_ERR_INVALID_ARG).
  * dX: dY scaled to fp16 per token (over all matrices), weight levels rounded
  * once to fp16, as mbok_gemm_gated; one fp32 sum over all matrices, rounded
  * once.  dalpha: products of the bf16 values are exact, sums fp32; the dense
- * M x N gradient is never stored.  Deterministic.  Bounded waits: bit 3 of
+ * M x N gradient is never stored; an infinite or NaN product makes the row's
+ * scales of that group NaN.  Deterministic.  Bounded waits: bit 3 of
  * mbok_read_device_errors. */
 int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* const* alpha, const int* K,
                        const int* M, int N, int group, const uint16_t* X, int T, const uint16_t* const* dY,
@@ -349,7 +358,9 @@ int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* 
  * that reads H, so that it need not be kept).
  *   dH, gate, up    : bf16 [T][M].
  *   dgate, dup, H   : out, bf16 [T][M], rounded once each; H may be NULL.  An
- *                     output may be one of the inputs (the same address).
+ *                     output may be one of the inputs (the same address) and
+ *                     must not overlap another array otherwise
+ *                     (MBOK_ERR_INVALID_ARG).
  * All 16-byte aligned.  1 <= T <= 2^23, 1 <= M <= 2^22. */
 int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t* up, int T, int M, uint16_t* dgate,
                         uint16_t* dup, uint16_t* H, void* stream);
@@ -376,7 +387,8 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
  *   weight  : fp32 [T], or NULL for 1.
  *   loss, lse : out, fp32 [T].
  *   dlogits : out, as logits with rows ld_dlogits apart, or NULL for the loss
- *             alone; may be `logits` itself (then with the same ld).
+ *             alone; may be `logits` itself (then with the same ld), and must
+ *             not share elements with it otherwise.
  * Sums are fp32 in a fixed order: deterministic.
  * 1 <= T <= 2^23, 1 <= V <= MBOK_DISTILL_MAX_VOCAB. */
 int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,

@@ -335,3 +335,27 @@ def test_gemm_backward_sizes_and_argument_errors(L):
     assert g(ws=None) == 6 and g(wsb=16) == 6 and g(ws=FAKE + 16) == 6
     with pytest.raises(ValueError):
         mb.gemm_backward([FAKE], [FAKE, FAKE], [1], [8], 128, 128, FAKE, 1, [FAKE], FAKE, None, None)
+
+
+def test_finetune_calls_refuse_overlapping_buffers(L):
+    # refused on the host before anything is launched; buffers that only touch are
+    # not (without a GPU such a call then fails to launch: MBOK_ERR_CUDA)
+    import torch
+    P, MB = 1 << 30, 1 << 20
+    g = lambda h, x, hd=1: L.mbok_gemv_gated(P, P, 3, P, P, 2, 64, 1024, 128, x, 1, 2, h, hd, P, MB, None)
+    assert g(P, P) == 1 and g(P + 4080, P) == 1 and g(P - 16, P) == 1 and g(P - 496, P, 0) == 1
+    b = lambda dh, gate, up, dg, du, H: L.mbok_gated_backward(dh, gate, up, 4, 64, dg, du, H, None)   # 512 bytes each
+    a = [P + i * MB for i in range(6)]
+    assert b(*a[:3], a[3], a[3], a[5]) == 1 and b(*a[:4], a[5] - 496, a[5]) == 1 and b(*a[:3], a[3], a[4], a[3] + 16) == 1
+    assert b(*a[:3], a[0] + 16, a[4], a[5]) == 1 and b(*a[:3], a[3], a[2] - 16, None) == 1
+    m = lambda H, gate, up: L.mbok_gemm_gated(P, P, 3, P, P, 2, 64, 1024, 128, P, 40, H, gate, up, P, 1 << 24, None)
+    assert m(a[0], a[0], a[1]) == 1 and m(a[0], a[1], a[1] + 16) == 1 and m(a[0], a[2], a[0] + 5104) == 1
+    arr = lambda *v: ctypes.cast((ctypes.c_void_p * len(v))(*v), ctypes.c_void_p)
+    ia = lambda *v: ctypes.cast((ctypes.c_int * len(v))(*v), ctypes.c_void_p)
+    back = lambda X, dY, dX, da: L.mbok_gemm_backward(2, arr(P, P), arr(P, P), ia(3, 2), ia(64, 40), 1024, 128, X, 40,
+                                                      arr(*dY), dX, da, P, 1 << 26, None)
+    assert back(a[0], a[1:3], a[0] + 81904, arr(a[3], None)) == 1          # X: 81920 bytes
+    assert back(a[0], a[1:3], a[2] - 16, arr(None, a[3])) == 1
+    if not torch.cuda.is_available():
+        assert g(P + 4096, P) == 5 and b(*a[:3], a[0], a[1], a[2]) == 5 and m(a[0], a[0] + 5120, a[0] + 10240) == 5
+        assert back(a[0], a[1:3], a[0], None) == 5                          # dX alone reads dY before it is written

@@ -498,6 +498,22 @@ def test_gemm_gated_many_tiles():
     _check_gated(gate, up, x64, _gemm_gated(gate, up, x_dev(x, "bf16"), True), True)
 
 
+@pytest.mark.parametrize("M,N,T", [(101, 2304, 633), (136, 2304, 21), (100, 4096, 300), (9600, 2048, 5)])
+def test_gemm_gated_cut_tiles(M, N, T):
+    # few or unevenly many tiles: runs of stages begin and end inside tiles, whose parts are added
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    up = lambda n, m: (n + m - 1) // m * m
+    assert mb.gemm_gated_workspace_bytes(M, N, T) > up(T * N * 2, 256) + up(up(T, 16) * 4, 256)
+    gate, upm = Layer(3, M, N, 131, pad_nan=True), Layer(2, M, N, 132, pad_nan=True)
+    x, x64 = _x(T, N, 133, "bf16")
+    X = x_dev(x, "bf16")
+    got = _gemm_gated(gate, upm, X, True)
+    _check_gated(gate, upm, x64, got, True)
+    again = _gemm_gated(gate, upm, X, False)
+    assert torch.equal(again[0], got[0])
+
+
 def test_gemm_gated_activation_range():
     # tokens of very different size, zeros, subnormals, infinities and NaN: a token's scale is its own
     import torch
@@ -602,6 +618,25 @@ def test_gemm_backward_runs_splits_and_tiles(M, N, T):
     import torch
     again = _gemm_backward(layers, X, dYs)
     assert torch.equal(first[0], again[0]) and all(torch.equal(a, b) for a, b in zip(first[1], again[1]))
+
+
+@pytest.mark.parametrize("spec,N,T", [([(2, 2764)], 128, 235), ([(2, 1499), (3, 213), (3, 64)], 1408, 21),
+                                      ([(1, 700), (4, 1300)], 256, 400)])
+def test_gemm_backward_cut_tiles(spec, N, T):
+    # as above, runs that begin and end in different matrices
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    Ks, Ms = [k for k, _ in spec], [m for _, m in spec]
+    up = lambda n, m: (n + m - 1) // m * m
+    base = sum(up(T * up(m, 8) * 2, 256) * (2 if m % 8 else 1) for m in Ms) + up(up(T, 16) * 4, 256)
+    assert mb.gemm_backward_workspace_bytes(Ks, Ms, N, T) > base
+    layers = [Layer(k, m, N, 141 + i, pad_nan=True) for i, (k, m) in enumerate(spec)]
+    X = x_dev(wl.x_normal(T, N, 143), "bf16")
+    dYs = [_grads(T, m.M, 144 + i) for i, m in enumerate(layers)]
+    first = _gemm_backward(layers, X, dYs)
+    _check_backward(layers, X, dYs, *first)
+    again = _gemm_backward(layers, X, dYs, want_a=[False] * len(spec))
+    assert torch.equal(first[0], again[0])
 
 
 def test_gemm_backward_parts():
