@@ -108,21 +108,23 @@ def _ptrs(*ts) -> list:
     raw device pointer).  Every tensor must be a contiguous CUDA tensor on the
     current device: the library launches there, and a pointer into another
     GPU's memory would be dereferenced by its kernels."""
-    dev = None
+    dev = None   # of the first tensor; the others' are compared with it at once
     out = []
     for t in ts:
         if t is None or isinstance(t, int):
             out.append(t)
             continue
-        if not t.is_cuda:
-            raise ValueError("MBOK operates on CUDA tensors only")
+        d = t.device
+        if d != dev:
+            if not t.is_cuda:
+                raise ValueError("MBOK operates on CUDA tensors only")
+            current = torch.cuda.current_device()
+            if d.index != current:
+                raise ValueError(f"tensor on {d} but the current device is cuda:{current}; "
+                                 "MBOK launches on the current device")
+            dev = d
         if not t.is_contiguous():
             raise ValueError("MBOK needs contiguous tensors")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError(f"tensor on {t.device} but the current device is cuda:{dev}; "
-                             "MBOK launches on the current device")
         out.append(t.data_ptr())
     return out
 
@@ -343,12 +345,14 @@ def gemm_backward(packed_list, alpha_list, K_list, M_list, N, group, X, T, dY_li
     if not (len(alpha_list) == len(K_list) == len(M_list) == len(dY_list) == len(dalpha_list) == n):
         raise ValueError("gemm_backward: one packed, alpha, K, M, dY and dalpha per matrix")
     ptrs = _ptrs(*packed_list, *alpha_list, *dY_list, *dalpha_list, X, dX, workspace)
-    array = ctypes.c_void_p * n
-    ints = ctypes.c_int * n
     px, pdx, pws = ptrs[4 * n:]
-    _check(lib().mbok_gemm_backward(n, array(*ptrs[:n]), array(*ptrs[n:2 * n]), ints(*K_list), ints(*M_list), N, group,
-                                    px, T, array(*ptrs[2 * n:3 * n]), pdx, array(*ptrs[3 * n:4 * n]), pws,
-                                    _ws_bytes(workspace), _stream(stream)), "mbok_gemm_backward")
+    arrays = (ctypes.c_void_p * (4 * n))(*ptrs[:4 * n])   # four host arrays of n pointers, one after another
+    at, step = ctypes.addressof(arrays), n * ctypes.sizeof(ctypes.c_void_p)
+    ints = (ctypes.c_int * (2 * n))(*K_list, *M_list)
+    ki = ctypes.addressof(ints)
+    _check(lib().mbok_gemm_backward(n, at, at + step, ki, ki + n * ctypes.sizeof(ctypes.c_int), N, group, px, T,
+                                    at + 2 * step, pdx, at + 3 * step, pws, _ws_bytes(workspace), _stream(stream)),
+           "mbok_gemm_backward")
 
 
 def gated_backward(dH, gate, up, T, M, dgate, dup, H=None, stream=None) -> None:
