@@ -16,7 +16,8 @@
 // gradient, which finds the row in L2 (five CTAs per SM hold rows of about 50 MB
 // in flight on the whole GPU at V = 32000 bf16, L2 is 126 MB).  Keeping the row
 // in registers between the passes instead left two CTAs per SM, too few to hide
-// one's loads behind the other's arithmetic: 2048 x 32000 bf16 took 109 us.
+// one's loads behind the other's arithmetic: 2048 x 32000 bf16 took 109 us against
+// 74.  Apart (1024 x 32000 fp32) loss and gradient take 69 us, 5.7 TB/s.
 // Each thread keeps a running (max, sum) pair of its own; one block step merges
 // them.  A ninth warp meanwhile forms the teacher's softmax from the list and
 // gathers the listed logits before anything is written, so dz may be the logits
@@ -607,6 +608,9 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // with it the pass needs no maxima, no rescaling and no list.  Where the sum
 // leaves 2^-60 .. 2^100 (or is NaN) the row is summed again from its maximum.
 // Only the last step needs the list: it is long in coming for the first row.
+// 2048 x 32000 bf16, loss and gradient: 59 us, 4.4 TB/s of logits and gradients
+// (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
+// issue slots 65 %: a row's two passes and their barriers take as long as its copies.
 constexpr int kRingSlots = 3;
 constexpr int kRingRowWarps = 24;
 constexpr int kRingRowThreads = kRingRowWarps * 32;

@@ -5,7 +5,7 @@
 // element.  Every thread takes vectors of 8 elements (16 bytes), two in flight
 // per array; the arithmetic is fp32 and each output is rounded once.  An output
 // may be one of the inputs: an element's inputs are read before its outputs are
-// written, by the same thread.
+// written, by the same thread.  11008 x 2048 with h: 44.3 us = 6.1 TB/s.
 #include "mbok_common.cuh"
 
 namespace mbok {

@@ -23,7 +23,8 @@
 //    of dalpha at 2048 tokens, 11008 x 4096: 2.6e-7 with runs of 256, 4.8e-7
 //    with 512, 1.0e-6 with 1024; fp32 products summed on the CUDA cores 4e-7).
 //    Shorter runs repeat the epilogue more often (gate and up of that size, K =
-//    3: 331 us with 256, 259 us with 512).
+//    3: 331 us with 256, 259 to 268 us = 1375 to 1425 TFLOP/s with 512, tensor
+//    pipe 73 % busy; 221 us at K = 1, where the signed sums hide entirely).
 //  * With few tiles the tokens are split over several pairs, whose sums land in
 //    the workspace ([split][dalpha]) and are added in order by a second kernel:
 //    deterministic.
@@ -96,7 +97,7 @@ __device__ __forceinline__ DaItem da_item(const DaParams& p, int i) {
 // a plus where bit b of w[k] is set, taken as twice the sum over the set bits
 // minus the sum over all.  A bit test and a predicated add are two instructions
 // per element and kernel on two pipes; flipping the sign took three, two of
-// them on the logic pipe (K = 3: 281 -> 259 us at the sizes above).
+// them on the logic pipe (K = 3, 2048 tokens: 281 -> 259 us).
 __device__ __forceinline__ void add_signed(const uint32_t v[32], const uint32_t w[MBOK_MAX_K], int K,
                                            float S[MBOK_MAX_K]) {
   float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
