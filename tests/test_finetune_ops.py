@@ -813,3 +813,90 @@ def test_distill_many_rows(dtype, V, T):
     mb.distill_loss(zd, _code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse, zd, V)
     torch.cuda.synchronize()
     assert torch.equal(zd, first)
+
+
+def _call_set(seed, T=150, batch=6):
+    """One of each call on inputs of a seed: functions that issue them, their outputs and what they read."""
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    M, N, V = 333, 2304, 3000
+    gate, up = Layer(3, M, N, 151), Layer(2, M, N, 152)
+    X = x_dev(wl.x_normal(T, N, seed), "bf16")
+    x = x_dev(wl.x_normal(batch, N, seed + 1), "bf16")
+    dYs = [_grads(T, M, seed + 2), _grads(T, M, seed + 3)]
+    Z = _grads(T, V, seed + 4, 2.0)
+    rng = np.random.default_rng(seed + 5)
+    teacher = to_dev(rng.standard_normal((T, 8)).astype(np.float32))
+    index = to_dev(rng.integers(0, V, (T, 8)).astype(np.int32))
+    e = lambda *shape, dt=torch.bfloat16: torch.zeros(shape, dtype=dt, device="cuda")
+    H, G, U, h, dX, dZ = e(T, M), e(T, M), e(T, M), e(batch, M), e(T, N), e(T, V)
+    das = [e(mb.alpha_elems(3, M, N), dt=torch.float32), e(mb.alpha_elems(2, M, N), dt=torch.float32)]
+    loss, lse = e(T, dt=torch.float32), e(T, dt=torch.float32)
+    dG, dU = e(T, M), e(T, M)
+    packed, alpha = [gate.packed, up.packed], [gate.blocked, up.blocked]
+
+    def issue(ws):
+        mb.gemm_gated(gate.packed, gate.blocked, 3, up.packed, up.blocked, 2, M, N, 128, X, T, H, G, U, ws[0])
+        mb.gemv_gated(gate.packed, gate.blocked, 3, up.packed, up.blocked, 2, M, N, 128, x, mb.BF16, batch, h, mb.BF16,
+                      ws[1])
+        mb.gated_backward(dYs[0], G, U, T, M, dG, dU)
+        mb.gemm_backward(packed, alpha, [3, 2], [M, M], N, 128, X, T, [dG, dYs[1]], dX, das, ws[2])
+        mb.distill_loss(Z, mb.BF16, T, V, V, teacher, index, 8, 1.5, None, loss, lse, dZ, V)
+
+    space = lambda: (mb.empty_gemm_gated_workspace(M, N, T), mb.empty_gated_workspace(3, 2, M, N, batch),
+                     mb.empty_gemm_backward_workspace([3, 2], [M, M], N, T))
+    return issue, [H, G, U, h, dG, dU, dX, *das, loss, lse, dZ], [X, x, *dYs, Z], space
+
+
+def test_calls_back_to_back_and_on_two_streams():
+    # launches that start before the preceding grid ends: two sets of calls in turn through one workspace, inputs
+    # overwritten right behind the calls, and two streams at once each with its own; always the bits of a call alone
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    sets = [_call_set(161), _call_set(171)]
+    want = []
+    for issue, outs, _, space in sets:
+        issue(space())
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+
+    def check():
+        torch.cuda.synchronize()
+        assert mb.read_device_errors() == 0
+        for (_, outs, _, _), w in zip(sets, want):
+            assert all(torch.equal(a, b) for a, b in zip(outs, w))
+            for o in outs:
+                o.zero_()
+        torch.cuda.synchronize()
+
+    shared = sets[0][3]()
+    for _ in range(5):
+        for issue, *_ in sets:
+            issue(shared)
+    check()
+    kept = [[t.clone() for t in ins] for _, _, ins, _ in sets]
+    for issue, _, ins, _ in sets:
+        issue(shared)
+        for t in ins:
+            t.fill_(float("nan"))
+    check()
+    for (_, _, ins, _), k in zip(sets, kept):
+        for t, v in zip(ins, k):
+            t.copy_(v)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = [s[3]() for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (issue, *_), stream, ws in zip(sets, streams, spaces):
+            with torch.cuda.stream(stream):
+                issue(ws)
+    check()
+    # captured together, replayed twice
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for issue, *_ in sets:
+            issue(shared)
+    for _ in range(2):
+        graph.replay()
+        check()
