@@ -8,6 +8,9 @@ source or header is newer than the library.
 build(variant="stamps") builds the profiling library libmbok_stamps.so from
 the same sources with MBOK_PHASE_STAMPS defined: the decode lookup kernels
 then record per-CTA phase timestamps (read by `bench.py --phase-profile`).
+
+csrc/marshal.cpp, the binding's argument marshalling, becomes the extension
+module boolean_weight_matmul_b200/_marshal.so (C++, against torch's headers).
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +28,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmbok.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 VARIANTS = {"": ("libmbok.so", []), "stamps": ("libmbok_stamps.so", ["-DMBOK_PHASE_STAMPS"])}
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -64,8 +70,34 @@ def _compile(src: str, verbose: bool, out_dir: str = BUILD_DIR, extra=()) -> str
     return obj
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile the extension module _marshal.so; returns its path."""
+    deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
+        return MARSHAL
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"]]
+    for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include")):
+        cmd += ["-isystem", d]
+    cmd += [MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:
-    """Compile and link libmbok.so (or a profiling variant); returns its path."""
+    """Compile and link libmbok.so (or a profiling variant) and the marshalling
+    module; returns the library's path."""
+    build_marshal(force)
     name, extra = VARIANTS[variant]
     lib = os.path.join(HERE, name)
     out_dir = os.path.join(BUILD_DIR, variant) if variant else BUILD_DIR

@@ -359,3 +359,48 @@ def test_finetune_calls_refuse_overlapping_buffers(L):
     if not torch.cuda.is_available():
         assert g(P + 4096, P) == 5 and b(*a[:3], a[0], a[1], a[2]) == 5 and m(a[0], a[0] + 5120, a[0] + 10240) == 5
         assert back(a[0], a[1:3], a[0], None) == 5                          # dX alone reads dY before it is written
+
+
+def test_marshalled_calls_convert_and_refuse(L):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    # raw pointers, ints and a raw stream reach the library, whose status comes back
+    for status, kw in ((2, dict(T=0)), (1, dict(dH=None)), (3, dict(up=FAKE + 2))):
+        a = dict(dH=FAKE, gate=FAKE, up=FAKE, T=4, M=64, dgate=FAKE, dup=FAKE, H=None, stream=0)
+        with pytest.raises(mb.MbokError) as e:
+            mb.gated_backward(**{**a, **kw})
+        assert e.value.status == status and "mbok_gated_backward" in str(e.value)
+    t = torch.zeros(64, dtype=torch.bfloat16)
+    two = [FAKE, FAKE]
+    back = lambda **kw: mb.gemm_backward(*[kw.get(k, v) for k, v in dict(
+        packed=two, alpha=two, K=[3, 2], M=(64, 40), N=1024, group=128, X=FAKE, T=40, dY=two, dX=FAKE, da=None, ws=None,
+        stream=0).items()])
+    with pytest.raises(mb.MbokError) as e:
+        back()
+    assert e.value.status == 6                                   # no workspace: every other argument passed
+    for kw, status in ((dict(K=[3, 5]), 1), (dict(M=[64, 0]), 2), (dict(packed=[FAKE, None]), 1), (dict(N=1000), 2),
+                       (dict(packed=[FAKE] * 9, alpha=[FAKE] * 9, K=[1] * 9, M=[8] * 9, dY=[FAKE] * 9), 1)):
+        with pytest.raises(mb.MbokError) as e:
+            back(**kw)
+        assert e.value.status == status
+    with pytest.raises(ValueError):
+        back(dY=[FAKE, t])                                       # a CPU tensor in a list
+    with pytest.raises(ValueError):
+        back(ws=t)
+    with pytest.raises(TypeError):
+        back(ws=FAKE)                                            # a workspace has a size
+    with pytest.raises(TypeError):
+        back(X="x")
+    with pytest.raises(TypeError):
+        back(K=[3, "x"])
+    with pytest.raises(OverflowError):
+        back(T=1 << 40)
+    with pytest.raises(OverflowError):
+        mb.distill_loss(FAKE, mb.F32, 1, 8, -1, FAKE, FAKE, 1, 1.0, None, FAKE, FAKE, stream=0)
+    with pytest.raises(TypeError):
+        mb.distill_backward(FAKE, mb.F32, 1, 8, 8, FAKE, FAKE, 1, "x", None, FAKE, None, FAKE, 8, 0)
+    with pytest.raises(mb.MbokError) as e:
+        mb.distill_backward(FAKE, mb.F32, 1, 8, 8, FAKE, FAKE, 1, float("nan"), None, FAKE, None, FAKE, 8, 0)
+    assert e.value.status == 1
+    with pytest.raises(TypeError):
+        mb._marshal().gated_backward(FAKE)                       # too few arguments

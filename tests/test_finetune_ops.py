@@ -900,3 +900,31 @@ def test_calls_back_to_back_and_on_two_streams():
     for _ in range(2):
         graph.replay()
         check()
+
+
+def test_marshalled_calls_check_tensors_and_take_streams():
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, M = 12, 40
+    a = [_grads(T, M, 181 + i) for i in range(3)]
+    out = [torch.zeros_like(a[0]) for _ in range(2)]
+    mb.gated_backward(*a, T, M, *out)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in out]
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, None):
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+        mb.gated_backward(*a, T, M, *out, stream=stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+    wide = torch.zeros((T, 2 * M), dtype=torch.bfloat16, device="cuda")[:, :M]
+    with pytest.raises(ValueError):
+        mb.gated_backward(wide, a[1], a[2], T, M, *out)
+    with pytest.raises(ValueError):
+        mb.gated_backward(a[0].cpu(), a[1], a[2], T, M, *out)
+    with torch.cuda.stream(side):                               # the current stream, while another one is busy
+        mb.gated_backward(a[0].data_ptr(), a[1], a[2], T, M, *out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(out, want))
