@@ -108,6 +108,7 @@ struct PairParams {
   int n;               // tokens per tile
   int naccs, n_acc;    // accumulators per tile (1 or 2) and tokens in each (multiple of 16, <= 256)
   int slots, wslots;   // ring slots, and those of bits and scales
+  int all_drain;       // the unpack warps share in every drain (always with two accumulators)
   int stages;          // per tile
   int row_tiles;       // tiles along W's rows (GATE, 128) or columns (GRAD, 256)
   int ntiles;
@@ -316,9 +317,17 @@ __device__ __forceinline__ void store_rows(bool pairs, uint16_t* out, int ld, in
   }
 }
 
-// silu(g) u for a bf16 result: the exponential and the quotient by the fast
-// approximations, a few 2^-22 of the value (and |g| 2^-23), far below its step.
-__device__ __forceinline__ float gated_fast(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+// silu(g) u for a bf16 result: g u / (1 + 2^(-g log2 e)) by the approximate
+// exponential and reciprocal, a few 2^-22 of the value (and |g| 2^-23), far below
+// its step.  Their forms that flush subnormals (the sigmoid's below g = -87 is 0)
+// need no range checks: 6 instructions a value, of which a drain has eight per
+// lane and 16 tokens.
+__device__ __forceinline__ float gated_fast(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
+  return g * r * u;
+}
 
 // Drain one warp's share of a finished tile whose first accumulator is at
 // `tmem`: lane quarter q, chunks of 16 tokens first, first + stride, ...
@@ -403,7 +412,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     }
     for (int b = 0; b < 2; ++b) {
       tc_mbar_init(&tfull[b], 1);
-      tc_mbar_init(&tempty[b], 2 * (p.naccs > 1 ? 4 + kPairUnpackWarps : 4));
+      tc_mbar_init(&tempty[b], 2 * (p.all_drain ? 4 + kPairUnpackWarps : 4));
     }
     tc_mbar_init(last_full, 1);
     s_fail = 0;
@@ -570,20 +579,23 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       }
       first = kb - it.k1;   // this group's first stage of the next item
       if (!ok) break;
-      // Two accumulators: every tile is drained by all warps.  One: only the
-      // last tile, on a barrier that completes once (a parity wait on tfull from
-      // here could pass on an earlier phase, since these warps do not wait for
-      // every tile).
+      // Two accumulators: a tile is drained by all warps before the next begins.
+      // One, and few stages per tile: behind the next tile's stages.  One, and
+      // many stages: only the last tile, on a barrier that completes once (a
+      // parity wait on tfull from here could pass on an earlier phase, since these
+      // warps do not wait for every tile).
       const bool last = i + 1 == n_mine;
-      if (p.naccs > 1 || last) {
-        if (!(p.naccs > 1 ? pair_wait(&tfull[0], unsigned(i) & 1u) : pair_wait(last_full, 0u))) { ok = false; break; }
+      const int d0 = p.naccs > 1 || (last && !p.all_drain) ? i : p.all_drain ? max(i - 1, 0) : i + 1;
+      const int d1 = p.naccs > 1 || last ? i : i - 1;
+      for (int j = d0; j <= d1 && ok; ++j) {
+        const int b = p.naccs > 1 ? 0 : j & 1, use = p.naccs > 1 ? j : j >> 1;
+        if (!(p.all_drain ? pair_wait(&tfull[b], unsigned(use) & 1u) : pair_wait(last_full, 0u))) { ok = false; break; }
         tc_fence_after();
-        const int b = p.naccs > 1 ? 0 : i & 1;
-        pair_drain<MODE>(p, tmem + uint32_t(b * 256), it, rank, warp & 3, lane,
+        pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair_item(p, walk, pair, j), rank, warp & 3, lane,
                          1 + (warp - kPairUnpackWarp0) / 4, 1 + kPairUnpackWarps / 4);
         tc_fence_before();
         __syncwarp();
-        if (p.naccs > 1 && lane == 0) pair_arrive(pair_leader(&tempty[0]));
+        if (p.all_drain && lane == 0) pair_arrive(pair_leader(&tempty[b]));
       }
     }
   } else {
@@ -592,7 +604,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       const int b = p.naccs > 1 ? 0 : i & 1, use = p.naccs > 1 ? i : i >> 1;
       if (!pair_wait(&tfull[b], unsigned(use) & 1u)) { ok = false; break; }
       tc_fence_after();
-      const bool shared = p.naccs > 1 || i + 1 == n_mine;   // with the unpack warps: every fifth chunk
+      const bool shared = p.all_drain || i + 1 == n_mine;   // with the unpack warps: every fifth chunk
       pair_drain<MODE>(p, tmem + uint32_t(b * 256), pair_item(p, walk, pair, i), rank, warp & 3, lane, 0,
                        shared ? 1 + kPairUnpackWarps / 4 : 1);
       tc_fence_before();
@@ -730,6 +742,10 @@ struct PairPlan {
 // 73 and 52 us, their dX for 256 tokens 185 and 67 us.
 constexpr int kPlanPairs = 74;
 constexpr int kPairMinRun = 4;   // stages
+// With fewer stages per tile than this the four epilogue warps do not keep up
+// with one accumulator, and the unpack warps drain too (1818 tokens, 2400 rows, N
+// = 128 and 512: 34 -> 21, 37 -> 24 us; at 16 and more no difference).
+constexpr int kPairFewStages = 16;
 static PairPlan pair_plan(int row_tiles, int stages, int T) {
   PairPlan best = {512, 0};
   double best_cost = -1;
@@ -776,6 +792,8 @@ static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t
   for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
   const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
   if (p.workers > pairs) p.workers = pairs;   // longer runs, whose sums take no more room
+  // (the stages of an item, in whole tiles or runs)
+  p.all_drain = p.naccs > 1 || (p.workers > 0 ? p.ntiles * p.stages / p.workers : p.stages) < kPairFewStages;
   if (p.workers > 0) {
     p.run = p.ntiles * p.stages / p.workers;
     p.run_rest = p.ntiles * p.stages % p.workers;
