@@ -66,9 +66,12 @@ constexpr int kPairOctets = 8;                                // row octets of a
 constexpr int kPairBits = 2 * kPairOctets * MBOK_MAX_K * 64;  // 4 KB: GATE two boxes of 64 bytes, GRAD one of 128
 constexpr int kPairAlpha = 2 * kPairOctets * MBOK_MAX_K * 16; // 1 KB
 constexpr int kPairWBytes = kPairBits + kPairAlpha;           // one slot of bits and scales
-// Ring slots hold A and this CTA's tokens (16 KB + 128 bytes per token): 4 for
-// tiles of 512 tokens, 6 for 256, 8 from 128 down.  Slots of bits and scales: 6
-// to 8.
+// Rings of A (16 KB a stage) and of this CTA's tokens (64 bytes per token of the
+// tile): 4 slots of each for tiles of 512 tokens, 8 and 4 for 256, 8 and 8 from
+// 128 down.  With a matrix of four kernels, whose unpack bounds the stages, 6 and
+// 3 for 512: 392 -> 373 us (K = 4, 11008 x 2 x 4096, 2048 tokens), where K = 3
+// goes 288 -> 295, its tokens arriving late.
+// Slots of bits and scales: 6 to 8.
 constexpr int kPairMaxSlots = 8;
 constexpr int kPairRing = 192 * 1024;
 constexpr int kPairBarriers = 512;
@@ -107,7 +110,7 @@ struct PairParams {
   int M, N, T;
   int n;               // tokens per tile
   int naccs, n_acc;    // accumulators per tile (1 or 2) and tokens in each (multiple of 16, <= 256)
-  int slots, wslots;   // ring slots, and those of bits and scales
+  int slots, xslots, wslots;   // ring slots of A, of tokens, of bits and scales
   int all_drain;       // the unpack warps share in every drain (always with two accumulators)
   int stages;          // per tile
   int row_tiles;       // tiles along W's rows (GATE, 128) or columns (GRAD, 256)
@@ -385,8 +388,9 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int x_bytes = p.n_acc / 2 * 128;                    // this CTA's tokens of one accumulator
-  const int slot_bytes = kPairABytes + p.naccs * x_bytes;   // A, then tokens
-  unsigned char* wring = smem + p.slots * slot_bytes;
+  const int xslot_bytes = p.naccs * x_bytes;
+  unsigned char* xring = smem + p.slots * kPairABytes;
+  unsigned char* wring = xring + p.xslots * xslot_bytes;
   uint64_t* wfull = reinterpret_cast<uint64_t*>(wring + p.wslots * kPairWBytes);   // bits and scales landed
   uint64_t* wempty = wfull + kPairMaxSlots;   // ... and unpacked
   uint64_t* ready = wempty + kPairMaxSlots;   // leader: both CTAs' tokens landed and their A is unpacked
@@ -436,8 +440,11 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   if (warp == 0) {
     // ---- token copies ----
     const unsigned bytes = unsigned(p.n * kPairBK * 2);   // both CTAs'
-    int s = 0, g = 0;
-    unsigned ph = 1;   // parity of the slot's previous use
+    // A stage's tokens arrive on the barrier of its A slot, and their slot is free
+    // once the stage xslots before is done (there are at least as many A slots, so
+    // that this stage's barrier is then through with its previous use).
+    int s = 0, xs = 0, es = 0, g = 0;   // A slot, token slot, A slot of stage g - xslots
+    unsigned eph = 0;
     for (int i = 0; i < n_mine && ok; ++i) {
       const PairItem it = pair_item(p, walk, pair, i);
       const int t0 = (it.tile / p.row_tiles) * p.n + rank * (p.n_acc / 2);
@@ -445,19 +452,23 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       if (MODE == kGrad)
         while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
       for (int kb = it.k0; kb < it.k1; ++kb, ++g) {
-        if (g >= p.slots && !pair_wait(&empty[s], ph)) { ok = false; break; }
+        if (g >= p.xslots) {
+          if (!pair_wait(&empty[es], eph)) { ok = false; break; }
+          if (++es == p.slots) { es = 0; eph ^= 1u; }
+        }
         const uint32_t bar = pair_leader(&ready[s]);
         const CUtensorMap* map = &maps.act[MODE == kGate ? 0 : m];
         if (elect_lane()) {
           if (rank == 0) tc_arrive_expect_tx(&ready[s], bytes);
-          unsigned char* x = smem + s * slot_bytes + kPairABytes;
+          unsigned char* x = xring + xs * xslot_bytes;
           const int k0 = (MODE == kGate ? kb : step) * kPairBK;
           pair_tma_load_2d(x, map, k0, t0, bar);
           if (p.naccs > 1) pair_tma_load_2d(x + x_bytes, map, k0, t0 + p.n_acc, bar);
         }
         __syncwarp();
         if (MODE == kGrad && ++step == p.mat[m].stages) { step = 0; ++m; }
-        if (++s == p.slots) { s = 0; ph ^= 1u; }
+        if (++s == p.slots) s = 0;
+        if (++xs == p.xslots) xs = 0;
       }
     }
   } else if (warp == 2) {
@@ -504,8 +515,8 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       constexpr int kAStep = MODE == kGate ? 32 >> 4 : 2048 >> 4;   // 16 k further in A
       const uint32_t base = tc_smem(smem);
       const uint64_t a0 = MODE == kGate ? tc_desc_sw128(base) : tc_desc_sw128_mn(base, 8192);
-      const uint64_t x0 = tc_desc_sw128(base + kPairABytes);
-      int s = 0;
+      const uint64_t x0 = tc_desc_sw128(tc_smem(xring));
+      int s = 0, xs = 0;
       unsigned ph = 0;
       for (int i = 0; i < n_mine && ok; ++i) {
         // one accumulator per tile: tiles alternate between two; else all tiles use both
@@ -517,11 +528,11 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         for (int kb = it.k0; kb < it.k1; ++kb) {
           if (!pair_wait(&ready[s], ph)) { ok = false; break; }
           tc_fence_after();
-          const uint64_t off = uint64_t((s * slot_bytes) >> 4);
+          const uint64_t aoff = uint64_t((s * kPairABytes) >> 4), xoff = uint64_t((xs * xslot_bytes) >> 4);
           if (elect_lane()) {
 #pragma unroll
             for (int kk = 0; kk < kPairBK / 16; ++kk) {
-              const uint64_t ad = a0 + off + uint64_t(kk * kAStep), xd = x0 + off + uint64_t(kk * (32 >> 4));
+              const uint64_t ad = a0 + aoff + uint64_t(kk * kAStep), xd = x0 + xoff + uint64_t(kk * (32 >> 4));
               const uint32_t acc = (kb > it.k0 || kk > 0) ? 1u : 0u;
               pair_mma(d, ad, xd, p.idesc, acc);
               if (p.naccs > 1) pair_mma(d + 256, ad, xd + uint64_t(x_bytes >> 4), p.idesc, acc);
@@ -534,6 +545,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
           }
           __syncwarp();
           if (++s == p.slots) { s = 0; ph ^= 1u; }
+          if (++xs == p.xslots) xs = 0;
         }
       }
     }
@@ -548,7 +560,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       int m = 0, kb = it.k0 + first, step = kb;
       for (; kb < it.k1; kb += kPairGroups, step += kPairGroups, g += kPairGroups) {
         const unsigned char* w = wring + ws * kPairWBytes;
-        unsigned char* a = smem + s * slot_bytes;
+        unsigned char* a = smem + s * kPairABytes;
         // the bits are there, and the slot's previous MMAs are done with its A
         if (!pair_wait(&wfull[ws], wph) || (g >= p.slots && !pair_wait(&empty[s], ph ^ 1u))) { ok = false; break; }
         if (MODE == kGate) {
@@ -785,12 +797,18 @@ template <PairMode MODE>
 static cudaError_t launch_pair(const PairMaps& maps, PairParams& p, cudaStream_t stream) {
   const int pairs = pair_count<MODE>();
   if (pairs < 1) return cudaErrorNotSupported;
-  const int slot_bytes = kPairABytes + p.n / 2 * 128;
-  p.slots = kPairRing / slot_bytes < kPairMaxSlots ? kPairRing / slot_bytes : kPairMaxSlots;
-  const int wslots = (kPairRings - p.slots * slot_bytes) / kPairWBytes;
+  const int xslot_bytes = p.n / 2 * 128;
+  int most_kernels = 0;
+  for (int i = 0; i < p.nmat; ++i) most_kernels = p.mat[i].K > most_kernels ? p.mat[i].K : most_kernels;
+  const int slots = (kPairRing - (most_kernels == 4 ? 3 : 4) * xslot_bytes) / kPairABytes;
+  p.slots = slots < kPairMaxSlots ? slots : kPairMaxSlots;
+  const int xslots = (kPairRing - p.slots * kPairABytes) / xslot_bytes;
+  p.xslots = xslots < p.slots ? xslots : p.slots;
+  const int ring = p.slots * kPairABytes + p.xslots * xslot_bytes;
+  const int wslots = (kPairRings - ring) / kPairWBytes;
   p.wslots = wslots < kPairMaxSlots ? wslots : kPairMaxSlots;
   for (int i = 0; i < 8; ++i) p.mul.pow2[i] = 1u << (15 - 2 * i);
-  const int smem = 1024 + p.slots * slot_bytes + p.wslots * kPairWBytes + kPairBarriers;
+  const int smem = 1024 + ring + p.wslots * kPairWBytes + kPairBarriers;
   if (p.workers > pairs) p.workers = pairs;   // longer runs, whose sums take no more room
   // (the stages of an item, in whole tiles or runs)
   p.all_drain = p.naccs > 1 || (p.workers > 0 ? p.ntiles * p.stages / p.workers : p.stages) < kPairFewStages;
