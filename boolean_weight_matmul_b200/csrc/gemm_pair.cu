@@ -48,9 +48,9 @@
 // flag, drains what it issued (bounded) and leaves with the other.
 //
 // Measured (LLaMA-7B gate and up, K = 3, 4096 columns, with the scaling pass):
-//   GATE  2048 tokens 281 us = 1315 TFLOP/s (a plain bf16 GEMM of the library
+//   GATE  2048 tokens 285 us = 1295 TFLOP/s (a plain bf16 GEMM of the library
 //         under the same load, which the power limit sets: 1354); tensor pipe
-//         64 % and ALU pipe 72 % busy.  K = 4: 376 us, bound by the unpack.
+//         64 % and ALU pipe 72 % busy.  K = 4: 366 to 375 us, bound by the unpack.
 //   GATE  256 tokens 81 us, 32 tokens 50 us: the unpack and the pipeline's fill.
 //   GRAD  2048 tokens 280 .. 300 us, 256 tokens 76 us.
 #include "scale_rows.h"
