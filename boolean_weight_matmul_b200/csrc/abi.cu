@@ -444,6 +444,11 @@ int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* 
   if (any && overlap(dX, x_bytes, X, x_bytes)) return MBOK_ERR_INVALID_ARG;
   for (int i = 0; i < nseg; ++i)
     if (any && overlap(dX, x_bytes, dY[i], size_t(T) * M[i] * 2)) return MBOK_ERR_INVALID_ARG;
+  // a matrix given twice has two gradients: they are not added up
+  for (int i = 0; any && i < nseg; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(dalpha[i], mbok_alpha_elems(K[i], M[i], N) * 4, dalpha[j], mbok_alpha_elems(K[j], M[j], N) * 4))
+        return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_gemm_backward(nseg, p8, alpha, shapes, X, T, dY, dX, dalpha, workspace, as_stream(stream)));
 }
 
@@ -468,6 +473,7 @@ int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, co
   if (dlogits != nullptr && ld_dlogits < size_t(V)) return MBOK_ERR_SHAPE;
   if (dlogits == logits && ld_dlogits != ld) return MBOK_ERR_SHAPE;   // in place: the same rows
   if (!aligned(weight, 4) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(dlogits, 16)) return MBOK_ERR_ALIGN;
+  if (overlap(loss, size_t(T) * 4, lse, size_t(T) * 4)) return MBOK_ERR_INVALID_ARG;
   return from_cuda(launch_distill_loss(logits, dtype == MBOK_F32, T, V, ld, teacher, index, top, temperature, weight,
                                        loss, lse, dlogits, ld_dlogits, as_stream(stream)));
 }

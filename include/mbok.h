@@ -340,7 +340,8 @@ size_t mbok_gemm_backward_workspace_bytes(int nseg, const int* K, const int* M, 
  *            (mbok_alpha_elems(K[s], M[s], N) elements, pad rows 0), or NULL;
  *            an entry may be NULL (a matrix whose scales are frozen).
  *   All 16-byte aligned; 1 <= T <= 2^23.  With dalpha asked for, dX must not
- *   overlap X or a dY (MBOK_ERR_INVALID_ARG).
+ *   overlap X or a dY, nor one dalpha another, also where a matrix is given
+ *   twice (MBOK_ERR_INVALID_ARG).
  * dX: dY scaled to fp16 per token (over all matrices), weight levels rounded
  * once to fp16, as mbok_gemm_gated; one fp32 sum over all matrices, rounded
  * once.  dalpha: products of the bf16 values are exact, sums fp32; the dense
@@ -385,7 +386,7 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
  *   teacher : fp32 [T][top].   index: int32 [T][top].   1 <= top <= MBOK_DISTILL_MAX_TOP.
  *   temperature : 2^-10 .. 2^10.
  *   weight  : fp32 [T], or NULL for 1.
- *   loss, lse : out, fp32 [T].
+ *   loss, lse : out, fp32 [T], not overlapping (MBOK_ERR_INVALID_ARG).
  *   dlogits : out, as logits with rows ld_dlogits apart, or NULL for the loss
  *             alone; may be `logits` itself (then with the same ld), and must
  *             not share elements with it otherwise.

@@ -356,7 +356,11 @@ def test_finetune_calls_refuse_overlapping_buffers(L):
                                                       arr(*dY), dX, da, P, 1 << 26, None)
     assert back(a[0], a[1:3], a[0] + 81904, arr(a[3], None)) == 1          # X: 81920 bytes
     assert back(a[0], a[1:3], a[2] - 16, arr(None, a[3])) == 1
+    assert back(a[0], a[1:3], a[3], arr(a[4], a[4])) == 1                  # one dalpha for two matrices
+    loss = lambda lo, ls: L.mbok_distill_loss(P, 0, 4, 100, 100, P, P, 8, 1.0, None, lo, ls, None, 0, None)
+    assert loss(a[0], a[0]) == 1 and loss(a[0], a[0] + 12) == 1
     if not torch.cuda.is_available():
+        assert loss(a[0], a[0] + 16) == 5
         assert g(P + 4096, P) == 5 and b(*a[:3], a[0], a[1], a[2]) == 5 and m(a[0], a[0] + 5120, a[0] + 10240) == 5
         assert back(a[0], a[1:3], a[0], None) == 5                          # dX alone reads dY before it is written
 
