@@ -51,7 +51,8 @@
 //   GATE  2048 tokens 285 us = 1295 TFLOP/s (a plain bf16 GEMM of the library
 //         under the same load, which the power limit sets: 1354); tensor pipe
 //         64 % and ALU pipe 72 % busy.  K = 4: 366 to 375 us, bound by the unpack.
-//   GATE  256 tokens 81 us, 32 tokens 50 us: the unpack and the pipeline's fill.
+//   GATE  256 tokens 62 us, 32 tokens 39 us (81 and 50 at the clocks that calls of
+//         2048 tokens leave): the unpack and the pipeline's fill.
 //   GRAD  2048 tokens 280 .. 300 us, 256 tokens 76 us.
 #include "scale_rows.h"
 #include "tc_pair.cuh"
@@ -430,15 +431,21 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
-  // What is above overlaps the preceding grid.  The scale gradients' kernel that
-  // may follow reads nothing that this one writes: it may start on idle SMs.
-  pdl_wait();
-  pdl_launch();
+  // This grid starts once every CTA of the scaling pass is past its own wait: all
+  // that came before that pass is complete, the weights among it, and their copies
+  // and unpack run beside it.  Tokens and what is read with the outputs wait for
+  // its end (three matrices, 130 and 382 tokens: 12.8 -> 11.7, 48 -> 45 us).
 
   // Every role walks the stages of all its tiles with a slot index and the
   // parity of the slot's current use.
   if (warp == 0) {
     // ---- token copies ----
+    if (elect_lane())
+      for (int m = 0; m < (MODE == kGate ? 1 : p.nmat); ++m) prefetch_map(&maps.act[m]);
+    pdl_wait();
+    // The scale gradients' kernel that may follow reads the scaling pass's copies
+    // and nothing that this one writes: it may start on idle SMs.
+    pdl_launch();
     const unsigned bytes = unsigned(p.n * kPairBK * 2);   // both CTAs'
     // A stage's tokens arrive on the barrier of its A slot, and their slot is free
     // once the stage xslots before is done (there are at least as many A slots, so
@@ -599,6 +606,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       const bool last = i + 1 == n_mine;
       const int d0 = p.naccs > 1 || (last && !p.all_drain) ? i : p.all_drain ? max(i - 1, 0) : i + 1;
       const int d1 = p.naccs > 1 || last ? i : i - 1;
+      if (d0 <= d1) pdl_wait();   // the tokens' scales
       for (int j = d0; j <= d1 && ok; ++j) {
         const int b = p.naccs > 1 ? 0 : j & 1, use = p.naccs > 1 ? j : j >> 1;
         if (!(p.all_drain ? pair_wait(&tfull[b], unsigned(use) & 1u) : pair_wait(last_full, 0u))) { ok = false; break; }
@@ -612,6 +620,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     }
   } else {
     // ---- epilogue: lane quarter warp & 3 ----
+    pdl_wait();   // the tokens' scales
     for (int i = 0; i < n_mine; ++i) {
       const int b = p.naccs > 1 ? 0 : i & 1, use = p.naccs > 1 ? i : i >> 1;
       if (!pair_wait(&tfull[b], unsigned(use) & 1u)) { ok = false; break; }

@@ -54,8 +54,8 @@ __device__ __forceinline__ uint32_t scaled_pair(uint32_t pair, float f) {
 __global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_constant__ ScaleRows p) {
   __shared__ uint32_t warp_max[kScaleThreads / 32];
   const size_t t = blockIdx.x;
-  pdl_launch();
   pdl_wait();   // the sources, and the workspace of an earlier call
+  pdl_launch();   // after the wait: the product that follows reads weights beside this grid
   uint32_t m = 0;
   for (int s = 0; s < p.nseg; ++s) {
     const ScaleSeg& g = p.seg[s];

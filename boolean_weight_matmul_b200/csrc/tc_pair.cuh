@@ -43,6 +43,10 @@ __device__ __forceinline__ void pair_tma_load_2d(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // As tc_wait, ordered after arrivals from either CTA.  A try may suspend the warp
 // for up to 20 us: many warps wait long, and their polling took issue slots from
 // the unpack (32 tokens, 11008 x 2 x 4096: 51 -> 49 us).
