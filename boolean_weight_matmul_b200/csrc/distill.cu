@@ -17,7 +17,8 @@
 // in flight on the whole GPU at V = 32000 bf16, L2 is 126 MB).  Keeping the row
 // in registers between the passes instead left two CTAs per SM, too few to hide
 // one's loads behind the other's arithmetic: 2048 x 32000 bf16 took 109 us against
-// 74.  Apart (1024 x 32000 fp32) loss and gradient take 69 us, 5.7 TB/s.
+// 74.  Apart (1024 x 32000 fp32) loss and gradient take 67 us, 5.8 TB/s.  All three
+// kernels start while the preceding grid ends (72 and 61 us without).
 // Each thread keeps a running (max, sum) pair of its own; one block step merges
 // them.  A ninth warp meanwhile forms the teacher's softmax from the list and
 // gathers the listed logits before anything is written, so dz may be the logits
@@ -454,6 +455,8 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
   const int per = (r.nvec + p.slices - 1) / p.slices;
   const int q0 = min(slice * per, r.nvec), q1 = min(q0 + per, r.nvec);
   const GradView d = grad_view<F32>(drow, r);
+  pdl_launch();
+  pdl_wait();   // nothing is read or written before the preceding grid is complete
 
   // the row's CTAs have all started once this barrier's wait returns (below,
   // before the first access to another CTA's shared memory)
@@ -558,6 +561,8 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
   const int per = (r.nvec + p.slices - 1) / p.slices;
   const int q0 = min(slice * per, r.nvec), q1 = min(q0 + per, r.nvec);
   const GradView d = grad_view<F32>(drow, r);
+  pdl_launch();
+  pdl_wait();
   uint4 v[kDistillVecs];
   if (warp < kDistillWarps) load_chunk<F32>(r, q0, q1, v);   // not waiting for the weight
   const float w = (p.weight != nullptr ? p.weight[t] : 1.f) * (p.grad != nullptr ? p.grad[t] : 1.f);
@@ -608,7 +613,7 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // with it the pass needs no maxima, no rescaling and no list.  Where the sum
 // leaves 2^-60 .. 2^100 (or is NaN) the row is summed again from its maximum.
 // Only the last step needs the list: it is long in coming for the first row.
-// 2048 x 32000 bf16, loss and gradient: 59 us, 4.4 TB/s of logits and gradients
+// 2048 x 32000 bf16, loss and gradient: 58 us, 4.5 TB/s of logits and gradients
 // (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
 // issue slots 65 %: a row's two passes and their barriers take as long as its copies.
 constexpr int kRingSlots = 3;
@@ -680,6 +685,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
   __syncthreads();
+  pdl_launch();
+  pdl_wait();
   auto row_of = [&](int i) { return size_t(blockIdx.x) + size_t(i) * gridDim.x; };
   auto logits_of = [&](size_t t) {
     return static_cast<const void*>(static_cast<const char*>(p.z) + t * p.ld * D::kBytes);
@@ -886,16 +893,16 @@ static cudaError_t launch_row(const DistillParams& p, int T, cudaStream_t stream
   cfg.gridDim = dim3(unsigned(T) * unsigned(p.slices));
   cfg.blockDim = dim3(kDistillBlock);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = unsigned(p.slices);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, distill_row_kernel<F32, WRITE>, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, distill_row_kernel<F32, WRITE>, p);
 }
 
 // Bytes of a ring slot: the row's vectors wherever it starts in its line.
@@ -917,8 +924,7 @@ static cudaError_t launch_ring(const DistillParams& d, int T, int slot, int smem
   rp.T = T;
   rp.slot_bytes = slot;
   const int sms = device_sm_count();
-  fn<<<unsigned(T < sms ? T : sms), kRingThreads, smem, stream>>>(rp);
-  return cudaGetLastError();
+  return launch_dependent(fn, dim3(unsigned(T < sms ? T : sms)), dim3(kRingThreads), size_t(smem), stream, rp);
 }
 
 // Reads and clears the ring kernel's error flag; ~0u if the read itself failed.
@@ -959,10 +965,8 @@ cudaError_t launch_distill_backward(const void* z, bool f32, int T, int V, size_
   p.dz = dz;
   p.ld_dz = ld_dz;
   p.slices = row_slices(T, V, f32, 1 << 20);
-  const unsigned grid = unsigned(T) * unsigned(p.slices);
-  if (f32) distill_grad_kernel<true><<<grid, kDistillBlock, 0, stream>>>(p);
-  else distill_grad_kernel<false><<<grid, kDistillBlock, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(f32 ? distill_grad_kernel<true> : distill_grad_kernel<false>,
+                          dim3(unsigned(T) * unsigned(p.slices)), dim3(kDistillBlock), 0, stream, p);
 }
 
 cudaError_t launch_distill_loss(const void* z, bool f32, int T, int V, size_t ld, const float* teacher,
