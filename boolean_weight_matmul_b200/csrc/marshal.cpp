@@ -61,7 +61,10 @@ class Args {
     items(i, n, [&](int k, PyObject* o) { out[k] = to_int(o); });
   }
   size_t size(int i) {
-    const size_t v = PyLong_AsSize_t(args_[i]);
+    PyObject* o = PyNumber_Index(args_[i]);
+    if (o == nullptr) throw Failed{};
+    const size_t v = PyLong_AsSize_t(o);
+    Py_DECREF(o);
     if (v == size_t(-1) && PyErr_Occurred()) throw Failed{};
     return v;
   }

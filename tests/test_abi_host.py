@@ -408,3 +408,8 @@ def test_marshalled_calls_convert_and_refuse(L):
     assert e.value.status == 1
     with pytest.raises(TypeError):
         mb._marshal().gated_backward(FAKE)                       # too few arguments
+    import numpy as np
+    with pytest.raises(mb.MbokError) as e:                       # numpy's integers as Python's
+        mb.distill_loss(FAKE, mb.F32, np.int64(1), np.int32(8), np.int64(7), FAKE, FAKE, 1, 1.0, None, FAKE, FAKE,
+                        stream=0)
+    assert e.value.status == 2
