@@ -287,8 +287,8 @@ size_t mbok_gemv_gated_workspace_bytes(int K_gate, int K_up, int M, int N, int b
  *   h must not overlap x (MBOK_ERR_INVALID_ARG).
  * One vector runs on the lookup kernel (one launch over both matrices and the
  * small launch that adds the slabs' partials and gates), two to 16 on the
- * tensor cores (one launch per 16 bf16 or 5 fp32 vectors, and for wide N a
- * small one that adds column slabs).
+ * tensor cores (one launch, and for wide N a small one that adds column slabs;
+ * fp32 vectors cost three bf16 ones).
  * g and u have the accuracy of mbok_gemv, with two vectors or more an absolute
  * error of 2^-31 of the vector's largest |x| per term besides; deterministic.
  * An infinite activation makes its vector's h NaN with two vectors or more.
