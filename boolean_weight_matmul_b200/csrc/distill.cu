@@ -21,8 +21,8 @@
 // kernels start while the preceding grid ends (72 and 61 us without).
 // Each thread keeps a running (max, sum) pair of its own; one block step merges
 // them.  A ninth warp meanwhile forms the teacher's softmax from the list and
-// gathers the listed logits before anything is written, so dz may be the logits
-// themselves.  Listed entries are few: their gradient is written over the dense
+// gathers the listed logits before any of them is written over, so dz may be the
+// logits themselves.  Listed entries are few: their gradient is written over the dense
 // pass's after a block barrier, with the p of equal indices added in list order.
 //
 // Arithmetic.  Everything runs in base 2, y = z log2(e) / tau, and a running sum
@@ -619,6 +619,10 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // 2048 x 32000 bf16, loss and gradient: 58 us, 4.5 TB/s of logits and gradients
 // (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
 // issue slots 65 %: a row's two passes and their barriers take as long as its copies.
+//
+// In place: a slot is copied out behind its list (done), and a row's ends, which no
+// copy moves, are written by the warp that waits for the list (the row warps, which
+// do not, would overwrite listed logits that a list warp has yet to gather).
 constexpr int kRingSlots = 3;
 constexpr int kRingRowWarps = 24;
 constexpr int kRingRowThreads = kRingRowWarps * 32;
@@ -760,8 +764,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
 #pragma unroll
           for (int j = 0; j < D::kVec; ++j) g[j] = 0.f;
         }
-        if (d.vec != nullptr && q >= r.qb && q < r.qe) vecs[q] = pack_vec<F32>(g);
-        else store_edge<F32>(d.row, q * D::kVec - r.a, r.V, pack_vec<F32>(g));
+        if (d.vec == nullptr) store_edge<F32>(d.row, q * D::kVec - r.a, r.V, pack_vec<F32>(g));   // never in place
+        else if (q >= r.qb && q < r.qe) vecs[q] = pack_vec<F32>(g);
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // generic writes -> bulk copy
       __syncwarp();
@@ -797,8 +801,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
       const float4 rs = row_sum[s];
       const float ref = rs.x, w = rs.z;
       uint4* vecs = reinterpret_cast<uint4*>(ring + s * rp.slot_bytes);
-      if (w != 0.f && teach.some() != 0) {
-        const float log2_sum = log2f(rs.y), inv = 1.f / rs.y, scale = w * p.inv_temp;
+      const bool used = w != 0.f && teach.some() != 0;
+      const float inv = 1.f / rs.y, scale = w * p.inv_temp;
+      if (d.vec != nullptr) {
+        // the row's ends, an element a lane: before the first whole vector, behind the last
+        const int head = r.qb == 0 ? 0 : min(D::kVec - r.a, r.V), tail = max(head, r.qe * D::kVec - r.a);
+        const int e = lane < head ? lane : tail + lane - head;
+        if (e < r.V)
+          store_elem<F32>(d.row, e, used ? scale * inv * exp_from<F32>(load_elem<F32>(r.row, e), ref, p) : 0.f);
+        __syncwarp();   // listed entries among them are written after
+      }
+      if (used) {
+        const float log2_sum = log2f(rs.y);
         for (int n = lane; n < p.top; n += 32) {
           float g;
           const int e = listed_grad<F32>(teach, r, 0, r.nvec, n, scale,
@@ -821,8 +835,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         }
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int q = lane; w != 0.f && q < r.nvec; q += 32) {
-          if (d.vec != nullptr && q >= r.qb && q < r.qe) vecs[q] = zero;
-          else store_edge<F32>(d.row, q * D::kVec - r.a, r.V, zero);
+          if (d.vec == nullptr) store_edge<F32>(d.row, q * D::kVec - r.a, r.V, zero);
+          else if (q >= r.qb && q < r.qe) vecs[q] = zero;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");

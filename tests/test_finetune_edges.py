@@ -1,0 +1,53 @@
+"""Calls of the gated, gradient and distillation operators that the documentation
+allows and that are easily got wrong: gradients in place, values near the ends of
+their type, masks, uneven batches.  Tolerances as in test_finetune_ops.py."""
+import numpy as np
+import pytest
+
+from oracle import finetune_oracle as F
+from helpers import ensure_built, guarded, to_dev
+import test_finetune_ops as ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    ensure_built()
+
+
+# ---- distillation in place -----------------------------------------------------
+
+@pytest.mark.parametrize("dtype,V,T,top,rounds", [("bf16", 2053, 1300, 512, 3), ("f32", 2053, 1300, 512, 3),
+                                                  ("bf16", 9, 2400, 9, 20), ("bf16", 17, 2400, 17, 20),
+                                                  ("bf16", 33, 1800, 33, 20), ("f32", 5, 2400, 5, 20),
+                                                  ("f32", 33, 1800, 33, 20)])
+def test_distill_in_place_with_listed_row_ends(dtype, V, T, top, rounds):
+    # many rows of every alignment, every element of their partial 16-byte vectors listed: the gradient written over
+    # the logits has the bits of the gradient written elsewhere, as have loss and lse
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    tau = 2.0
+    z, teacher, index, weight, _ = ops._distill_case(T, V, top, 31, dtype)
+    ends = np.concatenate([np.arange(8), np.arange(V - 8, V)]) if V > 33 else np.arange(V)[:top]
+    for t in range(4, T):   # at the end of the list, whose entries are gathered last
+        index[t, top - len(ends):] = np.roll(ends, t)
+    weight[5::11] = 0.0
+    index[6::11] = -1
+    td, xd, wd = to_dev(teacher), to_dev(index), to_dev(weight)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    dz = guarded((T, V), ops._dt(dtype))
+    mb.distill_loss(z.cuda(), ops._code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse, dz, V)
+    torch.cuda.synchronize()
+    ops._check_distill(z, teacher, index, weight, np.ones(T, dtype=np.float32), tau, V, dtype, ops._f64(loss),
+                       ops._f64(lse), ops._f64(dz))
+    for _ in range(rounds):
+        zd = z.cuda()
+        loss2, lse2 = torch.zeros_like(loss), torch.zeros_like(lse)
+        mb.distill_loss(zd, ops._code(dtype), T, V, V, td, xd, top, tau, wd, loss2, lse2, zd, V)
+        torch.cuda.synchronize()
+        assert mb.read_device_errors() == 0
+        assert torch.equal(zd, dz) and torch.equal(loss2, loss) and torch.equal(lse2, lse)
