@@ -54,6 +54,7 @@
 //   GATE  256 tokens 62 us, 32 tokens 39 us (81 and 50 at the clocks that calls of
 //         2048 tokens leave): the unpack and the pipeline's fill.
 //   GRAD  2048 tokens 280 .. 300 us, 256 tokens 76 us.
+#include "pair_ring.h"
 #include "scale_rows.h"
 #include "tc_pair.cuh"
 #include "tc_unpack.cuh"
@@ -72,13 +73,11 @@ constexpr int kPairWBytes = kPairBits + kPairAlpha;           // one slot of bit
 // 128 down.  With a matrix of four kernels, whose unpack bounds the stages, 6 and
 // 3 for 512: 392 -> 373 us (K = 4, 11008 x 2 x 4096, 2048 tokens), where K = 3
 // goes 288 -> 295, its tokens arriving late.
-// Slots of bits and scales: 6 to 8.
-constexpr int kPairMaxSlots = 8;
+// Slots of bits and scales: 6 to 8 (kPairMaxSlots, pair_ring.h).
 constexpr int kPairRing = 192 * 1024;
 constexpr int kPairBarriers = 512;
 constexpr int kPairSmemMax = 226 * 1024;   // of 227 KB, some of it static
 constexpr int kPairRings = kPairSmemMax - 1024 - kPairBarriers;
-constexpr int kPairGroups = 4;
 constexpr int kPairGroupWarps = 4;                            // 128 unpack threads per stage
 constexpr int kPairUnpackWarps = kPairGroups * kPairGroupWarps;
 constexpr int kPairUnpackWarp0 = 3;                           // after the two copy warps and the MMA warp
@@ -392,8 +391,8 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   const int xslot_bytes = p.naccs * x_bytes;
   unsigned char* xring = smem + p.slots * kPairABytes;
   unsigned char* wring = xring + p.xslots * xslot_bytes;
-  uint64_t* wfull = reinterpret_cast<uint64_t*>(wring + p.wslots * kPairWBytes);   // bits and scales landed
-  uint64_t* wempty = wfull + kPairMaxSlots;   // ... and unpacked
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(wring + p.wslots * kPairWBytes);   // a stage's bits and scales landed
+  uint64_t* wempty = wfull + kPairMaxSlots;   // ... and unpacked (both by pair_bits_barrier)
   uint64_t* ready = wempty + kPairMaxSlots;   // leader: both CTAs' tokens landed and their A is unpacked
   uint64_t* empty = ready + kPairMaxSlots;    // the stage's MMAs are done (both CTAs)
   uint64_t* tfull = empty + kPairMaxSlots;    // accumulator b holds a finished tile (both CTAs)
@@ -481,7 +480,6 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
   } else if (warp == 2) {
     // ---- copies of bits and scales ----
     int s = 0, g = 0;
-    unsigned ph = 1;
     for (int i = 0; i < n_mine && ok; ++i) {
       const PairItem it = pair_item(p, walk, pair, i);
       const int rt = it.tile % p.row_tiles;
@@ -489,31 +487,34 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
       if (MODE == kGrad)
         while (step >= p.mat[m].stages) step -= p.mat[m++].stages;
       for (int kb = it.k0; kb < it.k1; ++kb, ++g) {
-        if (g >= p.wslots && !pair_wait(&wempty[s], ph)) { ok = false; break; }
+        // the slot's last stage is unpacked
+        const int last = g - p.wslots;
+        if (last >= 0 && !pair_wait(&wempty[pair_bits_barrier(last)], pair_bits_parity(last))) { ok = false; break; }
         unsigned char* w = wring + s * kPairWBytes;
+        uint64_t* full = &wfull[pair_bits_barrier(g)];
         if (MODE == kGate) {
           const int o = (rt * 128 + rank * 64) / kOctet;
           if (elect_lane()) {
-            tc_arrive_expect_tx(&wfull[s], unsigned(p.mat[0].K + p.mat[1].K) * kPairOctets * (64 + 16));
+            tc_arrive_expect_tx(full, unsigned(p.mat[0].K + p.mat[1].K) * kPairOctets * (64 + 16));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int K = p.mat[i].K;
-              tc_tma_load_2d(w + i * (kPairBits / 2), &maps.bits[i], kb * 64, o * K, &wfull[s]);
-              tc_tma_load_2d(w + kPairBits + i * (kPairAlpha / 2), &maps.alpha[i], (kb / 2) * K * kOctet, o, &wfull[s]);
+              tc_tma_load_2d(w + i * (kPairBits / 2), &maps.bits[i], kb * 64, o * K, full);
+              tc_tma_load_2d(w + kPairBits + i * (kPairAlpha / 2), &maps.alpha[i], (kb / 2) * K * kOctet, o, full);
             }
           }
         } else {
           const int K = p.mat[m].K;
           const int j = rt * 256 + rank * 128;
           if (elect_lane()) {
-            tc_arrive_expect_tx(&wfull[s], unsigned(K) * kPairOctets * (128 + 16));
-            tc_tma_load_2d(w, &maps.bits[m], j, step * kPairOctets * K, &wfull[s]);
-            tc_tma_load_2d(w + kPairBits, &maps.alpha[m], (j / kGroup) * K * kOctet, step * kPairOctets, &wfull[s]);
+            tc_arrive_expect_tx(full, unsigned(K) * kPairOctets * (128 + 16));
+            tc_tma_load_2d(w, &maps.bits[m], j, step * kPairOctets * K, full);
+            tc_tma_load_2d(w + kPairBits, &maps.alpha[m], (j / kGroup) * K * kOctet, step * kPairOctets, full);
           }
           if (++step == p.mat[m].stages) { step = 0; ++m; }
         }
         __syncwarp();
-        if (++s == p.wslots) { s = 0; ph ^= 1u; }
+        if (++s == p.wslots) s = 0;
       }
     }
   } else if (warp == 1) {
@@ -561,7 +562,7 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
     const int grp = (warp - kPairUnpackWarp0) / kPairGroupWarps;
     const int gt = threadIdx.x - (kPairUnpackWarp0 + grp * kPairGroupWarps) * 32;
     int s = grp, ws = grp, g = grp, first = grp;   // both rings have at least kPairGroups slots
-    unsigned ph = 0, wph = 0;
+    unsigned ph = 0;
     for (int i = 0; i < n_mine && ok; ++i) {
       const PairItem it = pair_item(p, walk, pair, i);
       int m = 0, kb = it.k0 + first, step = kb;
@@ -569,7 +570,11 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         const unsigned char* w = wring + ws * kPairWBytes;
         unsigned char* a = smem + s * kPairABytes;
         // the bits are there, and the slot's previous MMAs are done with its A
-        if (!pair_wait(&wfull[ws], wph) || (g >= p.slots && !pair_wait(&empty[s], ph ^ 1u))) { ok = false; break; }
+        if (!pair_wait(&wfull[pair_bits_barrier(g)], pair_bits_parity(g)) ||
+            (g >= p.slots && !pair_wait(&empty[s], ph ^ 1u))) {
+          ok = false;
+          break;
+        }
         if (MODE == kGate) {
           switch (p.mat[gt >> 6].K) {   // the same for a whole warp
             case 1: unpack_gate<1>(w, a, p.mul, gt); break;
@@ -591,10 +596,10 @@ gemm_pair_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) {
           pair_arrive(pair_leader(&ready[s]));
-          tc_arrive(&wempty[ws]);
+          tc_arrive(&wempty[pair_bits_barrier(g)]);
         }
         if ((s += kPairGroups) >= p.slots) { s -= p.slots; ph ^= 1u; }
-        if ((ws += kPairGroups) >= p.wslots) { ws -= p.wslots; wph ^= 1u; }
+        if ((ws += kPairGroups) >= p.wslots) ws -= p.wslots;
       }
       first = kb - it.k1;   // this group's first stage of the next item
       if (!ok) break;
