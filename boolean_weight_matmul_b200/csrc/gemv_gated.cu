@@ -187,8 +187,9 @@ struct GdUnit {
         lo = gd_part(at(i) * scale, part) * f;
         hi = gd_part(at(i + 8) * scale, part) * f;
       } else {
-        lo = at(i) * (scale * f);
-        hi = at(i + 8) * (scale * f);
+        // the value scaled first: scale * f overflows where the vector is tiny
+        lo = at(i) * scale * f;
+        hi = at(i + 8) * scale * f;
       }
       const __half2 h = __floats2half2_rn(lo, hi);
       b[i] = *reinterpret_cast<const uint32_t*>(&h);

@@ -51,3 +51,28 @@ def test_distill_in_place_with_listed_row_ends(dtype, V, T, top, rounds):
         torch.cuda.synchronize()
         assert mb.read_device_errors() == 0
         assert torch.equal(zd, dz) and torch.equal(loss2, loss) and torch.equal(lse2, lse)
+
+
+# ---- gated decode ----------------------------------------------------------------
+
+@pytest.mark.parametrize("x_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("tiny", [1e-36, 2.0 ** -126, 2.0 ** -133])
+def test_gemv_gated_tiny_activations(x_dtype, tiny):
+    # activations far below one, subnormals among them, with zeros between: in all columns, and in one warp's 256
+    # columns alone; nothing becomes an infinity or NaN
+    import torch
+    K, M, N, batch = 2, 37, 512, 3
+    gate, up = ops.Layer(K, M, N, 201), ops.Layer(K, M, N, 202)
+    rng = np.random.default_rng(203)
+    for first in (0, 256):   # columns below `first` are ordinary
+        x = rng.standard_normal((batch, N))
+        x[:, first:] = np.sign(x[:, first:]) * tiny
+        x[:, first::3] = 0.0
+        xd = torch.from_numpy(x).to(ops._dt(x_dtype)).cuda()
+        x64 = ops._f64(xd)
+        assert (x64[:, first:] != 0).any()
+        h = ops._gemv_gated(gate, up, xd, x_dtype, batch, "f32")
+        g, Eg = F.project(gate.words, gate.alpha, K, M, N, x64)
+        u, Eu = F.project(up.words, up.alpha, K, M, N, x64)
+        want = F.silu(g) * u
+        ops._assert_within(ops._f64(h), want, ops._gated_tol(g, Eg, u, Eu, N * K, want, "f32"), f"{first}")
