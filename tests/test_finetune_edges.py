@@ -76,3 +76,28 @@ def test_gemv_gated_tiny_activations(x_dtype, tiny):
         u, Eu = F.project(up.words, up.alpha, K, M, N, x64)
         want = F.silu(g) * u
         ops._assert_within(ops._f64(h), want, ops._gated_tol(g, Eg, u, Eu, N * K, want, "f32"), f"{first}")
+
+
+@pytest.mark.parametrize("batch", [6, 7, 11, 13, 16])
+@pytest.mark.parametrize("M,N", [(70, 1664), (1300, 256), (129, 5248)])
+def test_gemv_gated_fp32_vectors_in_uneven_chunks(batch, M, N):
+    # fp32 vectors go in equal chunks of at most five, of which the last may be shorter: each vector has the bits of
+    # a call that brings it in a chunk of the same size
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    gate, up = ops.Layer(3, M, N, 211, pad_nan=True), ops.Layer(2, M, N, 212, pad_nan=True)
+    x, x64 = ops._x(batch, N, 213 + batch, "f32")
+    h = ops._gemv_gated(gate, up, to_dev(x), "f32", batch, "f32")
+    g, Eg = F.project(gate.words, gate.alpha, 3, M, N, x64)
+    u, Eu = F.project(up.words, up.alpha, 2, M, N, x64)
+    want = F.silu(g) * u
+    ops._assert_within(ops._f64(h), want, ops._gated_tol(g, Eg, u, Eu, N * 3, want, "f32"))
+    per = -(-batch // -(-batch // 5))
+    for v in range(0, batch, per):
+        n = min(per, batch - v)
+        if n < 2:
+            continue   # one vector takes the lookup kernel
+        if (3 * n <= 8) != (3 * per <= 8):
+            continue   # another tile width, whose warps take other columns
+        alone = ops._gemv_gated(gate, up, to_dev(x[v:v + n].copy()), "f32", n, "f32")
+        assert torch.equal(alone, h[v:v + n])
