@@ -568,9 +568,10 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
   pdl_wait();
   uint4 v[kDistillVecs];
   if (warp < kDistillWarps) load_chunk<F32>(r, q0, q1, v);   // not waiting for the weight
-  const float w = (p.weight != nullptr ? p.weight[t] : 1.f) * (p.grad != nullptr ? p.grad[t] : 1.f);
+  const float weight = p.weight != nullptr ? p.weight[t] : 1.f;
+  const float w = weight * (p.grad != nullptr ? p.grad[t] : 1.f);
   const float lse = p.lse_in[t];
-  if (w == 0.f) {
+  if (weight == 0.f || w == 0.f) {   // a weight of 0 also masks a gradient that is no number
     zero_row<F32>(d, r, q0, q1);
     return;
   }

@@ -399,7 +399,8 @@ int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, co
 /* The gradient alone, from the lse that mbok_distill_loss returned for the
  * same arguments and the gradient of the loss that followed:
  *     dlogits[t][j] = grad[t] weight[t] / tau (q_j - sum of p_i with index[t][i] = j),
- * q_j = exp(logits[t][j] / tau - lse[t]).  grad: fp32 [T], or NULL for 1.
+ * q_j = exp(logits[t][j] / tau - lse[t]).  grad: fp32 [T], or NULL for 1 (of a
+ * token of weight 0 or with nothing listed it may be anything).
  * Other arguments as mbok_distill_loss. */
 int mbok_distill_backward(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
                           const int32_t* index, int top, float temperature, const float* weight, const float* lse,

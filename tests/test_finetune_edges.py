@@ -101,3 +101,26 @@ def test_gemv_gated_fp32_vectors_in_uneven_chunks(batch, M, N):
             continue   # another tile width, whose warps take other columns
         alone = ops._gemv_gated(gate, up, to_dev(x[v:v + n].copy()), "f32", n, "f32")
         assert torch.equal(alone, h[v:v + n])
+
+
+# ---- distillation ------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_distill_weight_zero_masks_any_incoming_gradient(dtype):
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, V, top, tau = 8, 1003, 6, 2.0
+    z, teacher, index, weight, grad = ops._distill_case(T, V, top, 41, dtype, masked=False)
+    weight[:4] = 0.0
+    index[4] = -1
+    z[1, 5], z[2, :] = float("nan"), float("-inf")
+    grad[0], grad[1], grad[2], grad[4] = np.nan, np.inf, -np.inf, np.nan
+    td, xd, wd, gd = to_dev(teacher), to_dev(index), to_dev(weight), to_dev(grad)
+    loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+    mb.distill_loss(z.cuda(), ops._code(dtype), T, V, V, td, xd, top, tau, wd, loss, lse)
+    dz = guarded((T, V), ops._dt(dtype))
+    mb.distill_backward(z.cuda(), ops._code(dtype), T, V, V, td, xd, top, tau, wd, lse, gd, dz, V)
+    torch.cuda.synchronize()
+    assert (dz[:5] == 0).all() and (loss[:5] == 0).all()
+    ops._check_distill(z[5:], teacher[5:], index[5:], weight[5:], grad[5:], tau, V, dtype, ops._f64(loss[5:]),
+                       ops._f64(lse[5:]), ops._f64(dz[5:]))
