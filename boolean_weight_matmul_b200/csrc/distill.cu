@@ -25,16 +25,19 @@
 // logits themselves.  Listed entries are few: their gradient is written over the dense
 // pass's after a block barrier, with the p of equal indices added in list order.
 //
-// Arithmetic.  Everything runs in base 2, y = z log2(e) / tau, and a running sum
-// is kept as sum 2^(y - r) for a reference r that is the maximum logit's y
-// rounded to fp32: r is exact by definition (the sum belongs to it), so each
-// term costs one fused multiply-add and one exponential, and no rounding of the
-// maximum enters lse = (r + log2 sum) ln 2.  Sums, maxima and the softmax are
-// fp32.  For fp32 logits the factor log2(e) / tau is carried as two floats, so
-// that the exponent's error stays below the rounding of the result; bf16
-// gradients do not need the second one.
+// Arithmetic.  Everything runs in base 2, and a running sum is kept as
+// sum 2^((z - m) c), c = log2(e) / tau, for a reference m, the largest logit.  The
+// difference is taken first: it is exact near m, and the exponent is right, and
+// never above 0, wherever the logits lie.  (A multiply-add of z and the rounded m c,
+// one operation less, is off by that rounding: beyond 2^31 its power is an infinity,
+// also in a thread whose logits are all masked by a large negative number.  2048 x
+// 32000 bf16, loss alone: 27.8 us by multiply-adds, 29.0 by differences.)
+// lse = m / tau + ln sum.  Sums, maxima and the softmax are fp32.  The gradient
+// from a given lse, and the row ring, take multiply-adds: their reference is of
+// moderate size, or the row's result is limited by lse's own rounding anyway.
 #include <cooperative_groups.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "tc_common.cuh"
@@ -51,6 +54,7 @@ constexpr int kDistillVecs = 4;                                       // 16-byte
 constexpr int kDistillChunk = kDistillThreads * kDistillVecs;         // vectors per step of a CTA
 constexpr int kDistillMaxCluster = 8;
 constexpr float kNegInf = -INFINITY;
+constexpr float kLn2 = 0.693147182f;   // ln 2 rounded
 
 struct DistillParams {
   const void* z;
@@ -67,7 +71,8 @@ struct DistillParams {
   int V, top;
   int slices;               // CTAs per row
   float inv_temp;           // 1 / tau
-  float c2_hi, c2_lo;       // log2(e) / tau as a sum; c2_lo > 0
+  float c2;                 // log2(e) / tau rounded
+  float c2_hi, c2_lo;       // ... and as a sum; c2_lo > 0
 };
 
 template <bool F32>
@@ -84,12 +89,32 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// 2^(z log2(e) / tau - r).  c2_lo is positive, so that a logit of minus infinity
-// (masked) gives 0 and not NaN.
+// (z - m) log2(e) / tau, m finite.
+__device__ __forceinline__ float exponent(float z, float m, const DistillParams& p) { return (z - m) * p.c2; }
+__device__ __forceinline__ float exp_from(float z, float m, const DistillParams& p) { return ex2(exponent(z, m, p)); }
+
+// z log2(e) / tau - r, for |r| far below 2^24.  fp32 logits: log2(e) / tau as two
+// floats, so that the exponent's error stays at its rounding; bf16 gradients do not
+// need the second one.  c2_lo is positive, so that a logit of minus infinity
+// (masked) gives that and not NaN.
 template <bool F32>
-__device__ __forceinline__ float exp_from(float z, float r, const DistillParams& p) {
+__device__ __forceinline__ float exponent_near(float z, float r, const DistillParams& p) {
   const float y = fmaf(z, p.c2_hi, -r);
-  return ex2(F32 ? fmaf(z, p.c2_lo, y) : y);
+  return F32 ? fmaf(z, p.c2_lo, y) : y;
+}
+
+// Whether a row whose largest logit is m has a distribution: not if all are
+// masked (by -infinity or the type's lowest value), nor where m log2(e) / tau
+// overflows.
+template <bool F32>
+__device__ __forceinline__ bool has_distribution(float m, const DistillParams& p) {
+  const float lowest = F32 ? -FLT_MAX : __uint_as_float(0xFF7F0000u);
+  return m > lowest && fabsf(m * p.c2) < INFINITY;
+}
+
+// Natural logarithm of a sum that refers to the largest logit m.
+__device__ __forceinline__ float lse_of(float m, float log2_sum, const DistillParams& p) {
+  return fmaf(m, p.inv_temp, log2_sum * kLn2);
 }
 
 // Element i of a 16-byte vector as fp32.
@@ -317,21 +342,18 @@ __device__ __forceinline__ void teacher_softmax(const DistillParams& p, size_t t
   }
 }
 
-constexpr float kLn2 = 0.693147182f;   // ln 2 rounded
-
-// One warp: sum_i p_i (log p_i - log q_i) from the row's reference r and log2 of
-// its sum.  The two logarithms are subtracted entry by entry: their sums over
+// One warp: sum_i p_i (log p_i - log q_i) from log2 of the row's sum and the
+// exponents that refer to it, exponent_of(z).  The two logarithms are subtracted entry by entry: their sums over
 // the list are each far larger than the loss of a student that is close to its
 // teacher.
-template <bool F32>
-__device__ __forceinline__ float listed_loss(const DistillParams& p, const Teacher& s, float r, float log2_sum,
+template <class Y>
+__device__ __forceinline__ float listed_loss(const DistillParams& p, const Teacher& s, float log2_sum, Y exponent_of,
                                              int lane) {
   float sum = 0.f;
   for (int i = lane; i < p.top; i += 32) {
     if (s.idx(i) < 0) continue;
     const float prob = s.p(i);
-    const float y = fmaf(s.z(i), p.c2_hi, -r);
-    const float log2_q = (F32 ? fmaf(s.z(i), p.c2_lo, y) : y) - log2_sum;
+    const float log2_q = exponent_of(s.z(i)) - log2_sum;
     // an entry of probability 0 adds nothing, whatever the student's logit
     if (prob != 0.f) sum += prob * fmaf(-log2_q, kLn2, s.logp(i));
   }
@@ -342,10 +364,10 @@ __device__ __forceinline__ float listed_loss(const DistillParams& p, const Teach
 
 // Merge two (reference, sum) pairs; a pair without a logit above -infinity keeps
 // its sum as it is (0, or NaN from a NaN logit).
-__device__ __forceinline__ void merge(float& r, float& s, float r2, float s2) {
-  const float hi = fmaxf(r, r2);
-  s = (r == kNegInf ? s : s * ex2(r - hi)) + (r2 == kNegInf ? s2 : s2 * ex2(r2 - hi));
-  r = hi;
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, const DistillParams& p) {
+  const float hi = fmaxf(m, m2);
+  s = (m == kNegInf ? s : s * exp_from(m, hi, p)) + (m2 == kNegInf ? s2 : s2 * exp_from(m2, hi, p));
+  m = hi;
 }
 
 // The largest of a chunk's logits (NaN ignored; -infinity if there is none).
@@ -471,21 +493,21 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
       load_chunk<F32>(r, c0, q1, v);
       if (w == 0.f) break;   // the first loads did not wait for the weight
       // rescale the running sum where the reference grows
-      const float top = chunk_max<F32>(v) * p.c2_hi;
+      const float top = chunk_max<F32>(v);
       if (top > ref) {
-        s *= ex2(ref - top);   // 0 x 0 the first time
+        s *= exp_from(ref, top, p);   // 0 x 0 the first time
         ref = top;
       }
       const float from = ref == kNegInf ? 0.f : ref;
 #pragma unroll
       for (int i = 0; i < kDistillVecs; ++i)
 #pragma unroll
-        for (int j = 0; j < D::kVec; ++j) s += exp_from<F32>(vec_get<F32>(v[i], j), from, p);
+        for (int j = 0; j < D::kVec; ++j) s += exp_from(vec_get<F32>(v[i], j), from, p);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float r2 = __shfl_xor_sync(0xffffffffu, ref, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      merge(ref, s, r2, s2);
+      merge(ref, s, r2, s2, p);
     }
     if (lane == 0) warp_pair[warp] = make_float2(ref, s);
   }
@@ -497,7 +519,7 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
 #pragma unroll
     for (int o = kDistillWarps / 2; o > 0; o >>= 1) {
       const float r2 = __shfl_xor_sync(0xffffffffu, ref, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      merge(ref, s, r2, s2);
+      merge(ref, s, r2, s2, p);
     }
   }
   if (p.slices > 1) {
@@ -509,7 +531,7 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
     cluster.sync();
     ref = cta_pair[0].x;
     s = cta_pair[0].y;
-    for (int i = 1; i < p.slices; ++i) merge(ref, s, cta_pair[i].x, cta_pair[i].y);
+    for (int i = 1; i < p.slices; ++i) merge(ref, s, cta_pair[i].x, cta_pair[i].y, p);
   }
   // The next grid may start from here on: started with this one, its CTAs filled
   // the SMs unevenly where a grid is less than a wave (82 x 5591 fp32: 7.6 us, from
@@ -525,13 +547,13 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
     if (WRITE) zero_row<F32>(d, r, q0, q1);
     return;
   }
-  if (ref == kNegInf) s = NAN;   // no logit above -infinity: the row has no distribution
+  if (!has_distribution<F32>(ref, p)) s = NAN;
   if (slice == 0 && warp == kDistillWarps) {
     const float log2_sum = log2f(s);
-    const float sum = listed_loss<F32>(p, teach, ref, log2_sum, lane);
+    const float sum = listed_loss(p, teach, log2_sum, [&](float z) { return exponent(z, ref, p); }, lane);
     if (lane == 0) {
       p.loss[t] = w * sum;
-      p.lse[t] = (ref + log2_sum) * kLn2;
+      p.lse[t] = lse_of(ref, log2_sum, p);
     }
   }
   if (WRITE) {
@@ -540,11 +562,11 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
       for (int c0 = q0; c0 < q1; c0 += kDistillChunk) {
         uint4 v[kDistillVecs];
         load_chunk<F32>(r, c0, q1, v);
-        store_chunk<F32>(d, r, c0, q1, v, [&](float z) { return qs * exp_from<F32>(z, ref, p); });
+        store_chunk<F32>(d, r, c0, q1, v, [&](float z) { return qs * exp_from(z, ref, p); });
       }
     }
     __syncthreads();
-    patch_listed<F32>(p, teach, drow, r, q0, q1, scale, [&](float z) { return exp_from<F32>(z, ref, p) * inv; });
+    patch_listed<F32>(p, teach, drow, r, q0, q1, scale, [&](float z) { return exp_from(z, ref, p) * inv; });
   }
 }
 
@@ -617,7 +639,7 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // with it the pass needs no maxima, no rescaling and no list.  Where the sum
 // leaves 2^-60 .. 2^100 (or is NaN) the row is summed again from its maximum.
 // Only the last step needs the list: it is long in coming for the first row.
-// 2048 x 32000 bf16, loss and gradient: 58 us, 4.5 TB/s of logits and gradients
+// 2048 x 32000 bf16, loss and gradient: 59 us, 4.4 TB/s of logits and gradients
 // (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
 // issue slots 65 %: a row's two passes and their barriers take as long as its copies.
 //
@@ -661,6 +683,48 @@ __device__ __forceinline__ float row_reduce(float x, float* warp_val, int warp, 
   return all;
 }
 
+// Vector q of a row: from its slot, the row's ends from memory.
+template <bool F32>
+__device__ __forceinline__ uint4 ring_vec(const RowView& r, const uint4* vecs, int q) {
+  return q >= r.qb && q < r.qe ? vecs[q] : load_edge<F32>(r.row, q * DistillType<F32>::kVec - r.a, r.V);
+}
+
+// Put the gradients g of vector q in its slot; where the gradients' rows lie
+// otherwise than the logits' (never in place), in memory.  The row's ends follow
+// with the listed entries.
+template <bool F32>
+__device__ __forceinline__ void ring_put(const RowView& r, const GradView& d, uint4* vecs, int q, const float* g) {
+  if (d.vec == nullptr) store_edge<F32>(d.row, q * DistillType<F32>::kVec - r.a, r.V, pack_vec<F32>(g));
+  else if (q >= r.qb && q < r.qe) vecs[q] = pack_vec<F32>(g);
+}
+
+// The row warps' two passes for a row summed from its maximum m, a function of its
+// own: rare, and beside the others it would lengthen their loops.
+template <bool F32>
+__device__ __noinline__ float ring_sum_from(const DistillParams& p, RowView r, const uint4* vecs, float m) {
+  float s0 = 0.f, s1 = 0.f;
+  for (int q = threadIdx.x; q < r.nvec; q += kRingRowThreads) {
+    const uint4 v = ring_vec<F32>(r, vecs, q);
+#pragma unroll
+    for (int j = 0; j < DistillType<F32>::kVec; j += 2) {
+      s0 += exp_from(vec_get<F32>(v, j), m, p);
+      s1 += exp_from(vec_get<F32>(v, j + 1), m, p);
+    }
+  }
+  return s0 + s1;
+}
+template <bool F32>
+__device__ __noinline__ void ring_grad_from(const DistillParams& p, RowView r, GradView d, uint4* vecs, float m,
+                                            float qs) {
+  for (int q = threadIdx.x; q < r.nvec; q += kRingRowThreads) {
+    const uint4 v = ring_vec<F32>(r, vecs, q);
+    float g[DistillType<F32>::kVec];
+#pragma unroll
+    for (int j = 0; j < DistillType<F32>::kVec; ++j) g[j] = qs * exp_from(vec_get<F32>(v, j), m, p);
+    ring_put<F32>(r, d, vecs, q, g);
+  }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __grid_constant__ RingParams rp) {
   using D = DistillType<F32>;
@@ -671,7 +735,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
   __shared__ __align__(8) uint64_t done[kRingSlots];     // ... and its listed entries
   __shared__ __align__(8) uint64_t lfull[kRingLists], lempty[kRingLists];   // a list is ready, is read
   __shared__ __align__(16) float warp_val[3][kRingRowWarps];
-  __shared__ float4 row_sum[kRingSlots];                 // reference, sum, weight
+  __shared__ float4 row_sum[kRingSlots];                 // reference, sum, weight, whether summed from the maximum
   __shared__ int s_fail;                                 // a wait gave up: nothing more is stored
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tbytes = teacher_bytes(p.top);
@@ -720,53 +784,47 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
       const RowView r = row_view<F32>(logits_of(t), p.V);
       const GradView d = grad_view<F32>(grads_of(t), r);
       const float next_w = i + 1 < nrows ? weight_of(row_of(i + 1)) : 0.f;
-      // vector q of the row: from the slot, the row's ends from memory
-      auto vec_at = [&](int q) {
-        return q >= r.qb && q < r.qe ? vecs[q] : load_edge<F32>(r.row, q * D::kVec - r.a, r.V);
-      };
-      auto sum_from = [&](float ref) {
-        float s0 = 0.f, s1 = 0.f;
-        for (int q = gt; q < r.nvec; q += kRingRowThreads) {
-          const uint4 v = vec_at(q);
-#pragma unroll
-          for (int j = 0; j < D::kVec; j += 2) {
-            s0 += exp_from<F32>(vec_get<F32>(v, j), ref, p);
-            s1 += exp_from<F32>(vec_get<F32>(v, j + 1), ref, p);
-          }
-        }
-        return s0 + s1;
-      };
+      auto vec_at = [&](int q) { return ring_vec<F32>(r, vecs, q); };
       if (ok && !tc_wait(&full[s], unsigned(i / kRingSlots) & 1u)) failed();
       const bool used = w != 0.f;
-      float ref = 0.f;
-      float sum = row_reduce<false>(used ? sum_from(ref) : 1.f, warp_val[i & 1], warp, lane);
-      if (!(sum > 0x1p-60f && sum < 0x1p100f)) {   // the same for all: from the row's maximum
+      float s0 = 0.f, s1 = 0.f;
+      for (int q = gt; used && q < r.nvec; q += kRingRowThreads) {
+        const uint4 v = vec_at(q);
+#pragma unroll
+        for (int j = 0; j < D::kVec; j += 2) {
+          s0 += ex2(exponent_near<F32>(vec_get<F32>(v, j), 0.f, p));
+          s1 += ex2(exponent_near<F32>(vec_get<F32>(v, j + 1), 0.f, p));
+        }
+      }
+      float ref = 0.f, sum = row_reduce<false>(used ? s0 + s1 : 1.f, warp_val[i & 1], warp, lane);
+      const bool far = !(sum > 0x1p-60f && sum < 0x1p100f);   // the same for all
+      if (far) {   // from the row's maximum
         float m = kNegInf;
         for (int q = gt; q < r.nvec; q += kRingRowThreads) {
           const uint4 v = vec_at(q);
 #pragma unroll
           for (int j = 0; j < D::kVec; ++j) m = fmaxf(m, vec_get<F32>(v, j));
         }
-        ref = row_reduce<true>(m, warp_val[2], warp, lane) * p.c2_hi;
+        ref = row_reduce<true>(m, warp_val[2], warp, lane);
         row_sync();   // warp_val[i & 1] is read
-        // no logit above -infinity: the row has no distribution
-        sum = row_reduce<false>(ref == kNegInf ? NAN : sum_from(ref), warp_val[i & 1], warp, lane);
+        sum = row_reduce<false>(has_distribution<F32>(ref, p) ? ring_sum_from<F32>(p, r, vecs, ref) : NAN,
+                                warp_val[i & 1], warp, lane);
       }
-      if (gt == 0) row_sum[s] = make_float4(ref, sum, w, 0.f);
+      if (gt == 0) row_sum[s] = make_float4(ref, sum, w, far ? 1.f : 0.f);
       const float inv = 1.f / sum, qs = w * p.inv_temp * inv;
       // the gradient in the row's place; an unused row's is 0 whatever its logits
-      for (int q = gt; q < r.nvec; q += kRingRowThreads) {
+      if (far) ring_grad_from<F32>(p, r, d, vecs, ref, qs);
+      for (int q = gt; !far && q < r.nvec; q += kRingRowThreads) {
         float g[D::kVec];
         if (used) {
           const uint4 v = vec_at(q);
 #pragma unroll
-          for (int j = 0; j < D::kVec; ++j) g[j] = qs * exp_from<F32>(vec_get<F32>(v, j), ref, p);
+          for (int j = 0; j < D::kVec; ++j) g[j] = qs * ex2(exponent_near<F32>(vec_get<F32>(v, j), 0.f, p));
         } else {
 #pragma unroll
           for (int j = 0; j < D::kVec; ++j) g[j] = 0.f;
         }
-        if (d.vec == nullptr) store_edge<F32>(d.row, q * D::kVec - r.a, r.V, pack_vec<F32>(g));   // never in place
-        else if (q >= r.qb && q < r.qe) vecs[q] = pack_vec<F32>(g);
+        ring_put<F32>(r, d, vecs, q, g);
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // generic writes -> bulk copy
       __syncwarp();
@@ -801,6 +859,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
       const Teacher teach = list_of(i);
       const float4 rs = row_sum[s];
       const float ref = rs.x, w = rs.z;
+      const bool far = rs.w != 0.f;
+      auto y_of = [&](float z) { return far ? exponent(z, ref, p) : exponent_near<F32>(z, ref, p); };
       uint4* vecs = reinterpret_cast<uint4*>(ring + s * rp.slot_bytes);
       const bool used = w != 0.f && teach.some() != 0;
       const float inv = 1.f / rs.y, scale = w * p.inv_temp;
@@ -809,7 +869,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         const int head = r.qb == 0 ? 0 : min(D::kVec - r.a, r.V), tail = max(head, r.qe * D::kVec - r.a);
         const int e = lane < head ? lane : tail + lane - head;
         if (e < r.V)
-          store_elem<F32>(d.row, e, used ? scale * inv * exp_from<F32>(load_elem<F32>(r.row, e), ref, p) : 0.f);
+          store_elem<F32>(d.row, e, used ? scale * inv * ex2(y_of(load_elem<F32>(r.row, e))) : 0.f);
         __syncwarp();   // listed entries among them are written after
       }
       if (used) {
@@ -817,16 +877,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         for (int n = lane; n < p.top; n += 32) {
           float g;
           const int e = listed_grad<F32>(teach, r, 0, r.nvec, n, scale,
-                                         [&](float z) { return exp_from<F32>(z, ref, p) * inv; }, g);
+                                         [&](float z) { return ex2(y_of(z)) * inv; }, g);
           if (e < 0) continue;
           const int q = (e + r.a) / D::kVec;
           if (d.vec != nullptr && q >= r.qb && q < r.qe) store_elem<F32>(vecs, e + r.a, g);
           else store_elem<F32>(d.row, e, g);
         }
-        const float kl = listed_loss<F32>(p, teach, ref, log2_sum, lane);
+        const float kl = listed_loss(p, teach, log2_sum, y_of, lane);
         if (lane == 0) {
           p.loss[t] = w * kl;
-          p.lse[t] = (ref + log2_sum) * kLn2;
+          p.lse[t] = far ? lse_of(ref, log2_sum, p) : (ref + log2_sum) * kLn2;
         }
       } else {
         // no weight (the row warps wrote zeros), or nothing listed
@@ -967,7 +1027,7 @@ static DistillParams distill_params(const void* z, size_t ld, int V, const float
   p.inv_temp = 1.f / temperature;
   const double c2 = 1.4426950408889634 / double(temperature);
   // rounded down, and below c2 also where fp32 holds it: c2_lo stays positive
-  p.c2_hi = float(c2);
+  p.c2 = p.c2_hi = float(c2);
   if (double(p.c2_hi) >= c2) p.c2_hi = nextafterf(p.c2_hi, 0.f);
   p.c2_lo = float(c2 - double(p.c2_hi));
   return p;

@@ -124,3 +124,57 @@ def test_distill_weight_zero_masks_any_incoming_gradient(dtype):
     assert (dz[:5] == 0).all() and (loss[:5] == 0).all()
     ops._check_distill(z[5:], teacher[5:], index[5:], weight[5:], grad[5:], tau, V, dtype, ops._f64(loss[5:]),
                        ops._f64(lse[5:]), ops._f64(dz[5:]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,top,tau", [(6, 2053, 9, 1.0), (6, 2053, 9, 2.0), (3, 40000, 9, 8.0), (640, 2053, 9, 2.0),
+                                         (640, 515, 9, 1.0)])
+def test_distill_masked_by_large_negative_logits(dtype, T, V, top, tau):
+    # blocks of logits masked by the lowest value and by other large negative numbers, more than one thread's share:
+    # probability 0 at every temperature; a row where nothing else is left has no distribution
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    z, teacher, index, weight, _ = ops._distill_case(T, V, top, 51, dtype, masked=False)
+    index = np.stack([np.random.default_rng(52 + t).permutation(V // 4)[:top] for t in range(T)]).astype(np.int32)
+    clean = z.clone()
+    masks = [torch.finfo(z.dtype).min, -1e30, -1e10, -3e9]
+    for t in range(T - 1):
+        first = V // 4 + (37 * t) % (V // 2)
+        z[t, first:first + V // 4] = masks[t % 4]
+        clean[t, first:first + V // 4] = float("-inf")
+    z[T - 1] = torch.finfo(z.dtype).min
+    td, xd, wd = to_dev(teacher), to_dev(index), to_dev(weight)
+    loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), ops._dt(dtype))
+    ones = np.ones(T, dtype=np.float32)
+    args = (z.cuda(), ops._code(dtype), T, V, V, td, xd, top, tau, wd)
+    mb.distill_loss(*args, loss, lse, dz, V)
+    dz2 = guarded((T, V), ops._dt(dtype))
+    mb.distill_backward(*args, lse, None, dz2, V)
+    torch.cuda.synchronize()
+    for d in (dz, dz2):
+        ops._check_distill(clean[:-1], teacher[:-1], index[:-1], weight[:-1], ones[:-1], tau, V, dtype,
+                           ops._f64(loss[:-1]), ops._f64(lse[:-1]), ops._f64(d[:-1]))
+        assert torch.isnan(loss[-1]) and torch.isnan(d[-1]).all()
+
+
+@pytest.mark.parametrize("T", [4, 640])
+def test_distill_huge_logits(T):
+    # logits whose step is many units: all probability on the largest, shared where there are several; the gradient
+    # has the ordinary relative error, since the differences of such logits are exact
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    V, top, tau = 1031, 5, 1.5
+    _, teacher, index, _, _ = ops._distill_case(T, V, top, 61, "f32", masked=False)
+    rng = np.random.default_rng(62)
+    for sign in (1.0, -1.0):
+        z = torch.from_numpy(sign * 2.0 ** 34 + 4096.0 * rng.integers(0, 3, (T, V))).float()
+        loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), torch.float32)
+        mb.distill_loss(z.cuda(), mb.F32, T, V, V, to_dev(teacher), to_dev(index), top, tau, None, loss, lse, dz, V)
+        torch.cuda.synchronize()
+        ones = np.ones(T)
+        want_loss, want_lse, want, q, p = F.distill(z.double().numpy(), teacher.astype(np.float64), index, tau, ones, ones)
+        # exponents of the largest are 0; the teacher's are off by 2^-24 of at most 16, and its sum by top 2^-24
+        ops._assert_within(ops._f64(dz), want, (q + p) / tau * 2.0 ** -18 + 1e-38, "dz")
+        # the loss is sum p (m - z) / tau and ordinary terms: a few roundings of each
+        ops._assert_within(ops._f64(loss), want_loss, np.abs(want_loss) * 2.0 ** -20 + 1e-4, "loss")
+        ops._assert_within(ops._f64(lse), want_lse, np.abs(want_lse) * 2.0 ** -22, "lse")
