@@ -370,13 +370,13 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, co
   m = hi;
 }
 
-// The largest of a chunk's logits (NaN ignored; -infinity if there is none).
-template <bool F32>
-__device__ __forceinline__ float chunk_max(const uint4 v[kDistillVecs]) {
+// The largest of n vectors' logits (NaN ignored; -infinity if there is none).
+template <bool F32, int n>
+__device__ __forceinline__ float vecs_max(const uint4* v) {
   if constexpr (F32) {
     float m = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kDistillVecs; ++i)
+    for (int i = 0; i < n; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) m = fmaxf(m, vec_get<true>(v[i], j));
     return m;
@@ -384,7 +384,7 @@ __device__ __forceinline__ float chunk_max(const uint4 v[kDistillVecs]) {
     const uint32_t none = 0xFF80FF80u;
     __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&none);
 #pragma unroll
-    for (int i = 0; i < kDistillVecs; ++i) {
+    for (int i = 0; i < n; ++i) {
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[j]));
@@ -493,7 +493,7 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
       load_chunk<F32>(r, c0, q1, v);
       if (w == 0.f) break;   // the first loads did not wait for the weight
       // rescale the running sum where the reference grows
-      const float top = chunk_max<F32>(v);
+      const float top = vecs_max<F32, kDistillVecs>(v);
       if (top > ref) {
         s *= exp_from(ref, top, p);   // 0 x 0 the first time
         ref = top;
@@ -634,12 +634,17 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // overlap all the time, which rows on independent CTAs do not: those start
 // together and stay in step.
 //
-// The reference of a row's sum is 0 instead of the maximum: any reference serves
-// from which no term overflows and the sum stays far above what vanishes, and
-// with it the pass needs no maxima, no rescaling and no list.  Where the sum
-// leaves 2^-60 .. 2^100 (or is NaN) the row is summed again from its maximum.
+// The reference of a row's sum is not its maximum but that of 32 vectors spread over
+// it, which the slot's copy warp finds, rounded to a whole exponent: any reference
+// serves from which no term overflows and no exponent is so large that its rounding
+// counts, and with it the pass needs no maxima, no rescaling and no list.  Whole
+// exponents are exact to add, so that the sum is then taken to one in [1, 2) and
+// every further exponent refers to that: rounded where it is small, wherever the
+// logits lie.  Where the sum leaves 2^-32 .. 2^32 (exponents of up to 32, rounded by
+// 2^-20) or is NaN, the row is summed again from its maximum.  (From 0, without a
+// maximum, exponents of rows at 69 were off by 2^-18 and losses by 4e-6.)
 // Only the last step needs the list: it is long in coming for the first row.
-// 2048 x 32000 bf16, loss and gradient: 59 us, 4.4 TB/s of logits and gradients
+// 2048 x 32000 bf16, loss and gradient: 59.5 us, 4.4 TB/s of logits and gradients
 // (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
 // issue slots 65 %: a row's two passes and their barriers take as long as its copies.
 //
@@ -655,6 +660,7 @@ constexpr int kRingEndWarp = kRingListWarp0 + kRingLists;
 constexpr int kRingCopyWarp0 = kRingEndWarp + 1;
 constexpr int kRingThreads = (kRingCopyWarp0 + kRingSlots) * 32;
 constexpr int kRingSmemMax = 224 * 1024;
+constexpr float kRingFarthest = 0x1p20f;   // references' magnitude: whole numbers, exact to add
 
 static __device__ unsigned int g_distill_error;
 
@@ -698,6 +704,19 @@ __device__ __forceinline__ void ring_put(const RowView& r, const GradView& d, ui
   else if (q >= r.qb && q < r.qe) vecs[q] = pack_vec<F32>(g);
 }
 
+// One warp: the reference of a row's first sum, the largest logit among 32 vectors
+// spread over the row, as a whole exponent; 0 if all are masked.
+template <bool F32>
+__device__ __forceinline__ float ring_reference(const DistillParams& p, const RowView& r, const uint4* vecs, int lane) {
+  float y = kNegInf;
+  if (r.qe > r.qb) {
+    const uint4 v = vecs[r.qb + lane * (r.qe - r.qb) / 32];
+    y = rintf(vecs_max<F32, 1>(&v) * p.c2_hi);
+  }
+  const int high = __reduce_max_sync(0xffffffffu, int(fminf(fmaxf(y, -kRingFarthest), kRingFarthest)));
+  return high == int(-kRingFarthest) ? 0.f : float(high);
+}
+
 // The row warps' two passes for a row summed from its maximum m, a function of its
 // own: rare, and beside the others it would lengthen their loops.
 template <bool F32>
@@ -731,10 +750,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
   const DistillParams& p = rp.d;
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) uint64_t full[kRingSlots];     // a slot's row landed
+  __shared__ __align__(8) uint64_t ready[kRingSlots];    // ... and its reference is found
   __shared__ __align__(8) uint64_t dense[kRingSlots];    // its dense gradient stands in the slot
   __shared__ __align__(8) uint64_t done[kRingSlots];     // ... and its listed entries
   __shared__ __align__(8) uint64_t lfull[kRingLists], lempty[kRingLists];   // a list is ready, is read
   __shared__ __align__(16) float warp_val[3][kRingRowWarps];
+  __shared__ float row_from[kRingSlots];                 // the first sum's reference
   __shared__ float4 row_sum[kRingSlots];                 // reference, sum, weight, whether summed from the maximum
   __shared__ int s_fail;                                 // a wait gave up: nothing more is stored
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -745,6 +766,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
   if (threadIdx.x == 0) {
     for (int s = 0; s < kRingSlots; ++s) {
       tc_mbar_init(&full[s], 1);
+      tc_mbar_init(&ready[s], 1);
       tc_mbar_init(&dense[s], kRingRowWarps);
       tc_mbar_init(&done[s], 1);
     }
@@ -785,20 +807,24 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
       const GradView d = grad_view<F32>(grads_of(t), r);
       const float next_w = i + 1 < nrows ? weight_of(row_of(i + 1)) : 0.f;
       auto vec_at = [&](int q) { return ring_vec<F32>(r, vecs, q); };
-      if (ok && !tc_wait(&full[s], unsigned(i / kRingSlots) & 1u)) failed();
+      if (ok && !tc_wait(&ready[s], unsigned(i / kRingSlots) & 1u)) failed();
       const bool used = w != 0.f;
-      float s0 = 0.f, s1 = 0.f;
+      float s0 = 0.f, s1 = 0.f, from = row_from[s];
       for (int q = gt; used && q < r.nvec; q += kRingRowThreads) {
         const uint4 v = vec_at(q);
 #pragma unroll
         for (int j = 0; j < D::kVec; j += 2) {
-          s0 += ex2(exponent_near<F32>(vec_get<F32>(v, j), 0.f, p));
-          s1 += ex2(exponent_near<F32>(vec_get<F32>(v, j + 1), 0.f, p));
+          s0 += ex2(exponent_near<F32>(vec_get<F32>(v, j), from, p));
+          s1 += ex2(exponent_near<F32>(vec_get<F32>(v, j + 1), from, p));
         }
       }
-      float ref = 0.f, sum = row_reduce<false>(used ? s0 + s1 : 1.f, warp_val[i & 1], warp, lane);
-      const bool far = !(sum > 0x1p-60f && sum < 0x1p100f);   // the same for all
-      if (far) {   // from the row's maximum
+      float ref = from, sum = row_reduce<false>(used ? s0 + s1 : 1.f, warp_val[i & 1], warp, lane);
+      const bool far = !(sum > 0x1p-32f && sum < 0x1p32f);   // the same for all; a NaN is far
+      if (!far) {   // the sum in [1, 2)
+        const uint32_t bits = __float_as_uint(sum);
+        ref += float(int(bits >> 23) - 127);
+        sum = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+      } else {   // from the row's maximum
         float m = kNegInf;
         for (int q = gt; q < r.nvec; q += kRingRowThreads) {
           const uint4 v = vec_at(q);
@@ -819,7 +845,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         if (used) {
           const uint4 v = vec_at(q);
 #pragma unroll
-          for (int j = 0; j < D::kVec; ++j) g[j] = qs * ex2(exponent_near<F32>(vec_get<F32>(v, j), 0.f, p));
+          for (int j = 0; j < D::kVec; ++j) g[j] = qs * ex2(exponent_near<F32>(vec_get<F32>(v, j), ref, p));
         } else {
 #pragma unroll
           for (int j = 0; j < D::kVec; ++j) g[j] = 0.f;
@@ -907,8 +933,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         tc_arrive(&lempty[i % kRingLists]);
       }
     }
-  } else if (lane == 0) {
-    // ---- a slot's copies ----
+  } else {
+    // ---- a slot's copies (its first lane), and its row's reference ----
     const int s = warp - kRingCopyWarp0;
     unsigned char* slot = ring + s * rp.slot_bytes;
     float w = s < nrows ? weight_of(row_of(s)) : 0.f;
@@ -918,17 +944,26 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
       const GradView d = grad_view<F32>(grads_of(t), r);
       const uint32_t bytes = r.qe > r.qb ? uint32_t(r.qe - r.qb) * 16 : 0u;
       const bool wanted = bytes > 0 && w != 0.f;
-      tc_arrive_expect_tx(&full[s], wanted ? bytes : 0u);
-      if (wanted)
-        asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                tc_smem(slot + r.qb * 16)),
-            "l"(r.vec + r.qb), "r"(bytes), "r"(tc_smem(&full[s]))
-            : "memory");
+      if (lane == 0) {
+        tc_arrive_expect_tx(&full[s], wanted ? bytes : 0u);
+        if (wanted)
+          asm volatile(
+              "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                  tc_smem(slot + r.qb * 16)),
+              "l"(r.vec + r.qb), "r"(bytes), "r"(tc_smem(&full[s]))
+              : "memory");
+      }
       if (i + kRingSlots < nrows) w = weight_of(row_of(i + kRingSlots));
+      if (!tc_wait(&full[s], unsigned(u) & 1u)) failed();
+      __syncwarp();
+      const float from = wanted ? ring_reference<F32>(p, r, reinterpret_cast<const uint4*>(slot), lane) : 0.f;
+      if (lane == 0) {
+        row_from[s] = from;
+        tc_arrive(&ready[s]);
+      }
       if (!tc_wait(&done[s], unsigned(u) & 1u)) failed();
-      if (*reinterpret_cast<volatile int*>(&s_fail) != 0) break;
-      if (bytes > 0 && d.vec != nullptr) {
+      if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_fail) != 0)) break;
+      if (lane == 0 && bytes > 0 && d.vec != nullptr) {
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(d.vec + r.qb),
                      "r"(tc_smem(slot + r.qb * 16)), "r"(bytes)
                      : "memory");
@@ -936,8 +971,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
         // the slot may be filled again once the copy has read it
         asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
       }
+      __syncwarp();
     }
-    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
   if (!ok) {
     // record it, and let this CTA's copies in land (bounded) before it leaves

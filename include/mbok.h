@@ -390,7 +390,8 @@ int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t
  *   dlogits : out, as logits with rows ld_dlogits apart, or NULL for the loss
  *             alone; may be `logits` itself (then with the same ld), and must
  *             not share elements with it otherwise.
- * Sums are fp32 in a fixed order: deterministic.
+ * Sums are fp32 in a fixed order: deterministic.  A probability below 2^-126 may
+ * come out as 0.
  * 1 <= T <= 2^23, 1 <= V <= MBOK_DISTILL_MAX_VOCAB. */
 int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
                       const int32_t* index, int top, float temperature, const float* weight, float* loss, float* lse,

@@ -178,3 +178,76 @@ def test_distill_huge_logits(T):
         # the loss is sum p (m - z) / tau and ordinary terms: a few roundings of each
         ops._assert_within(ops._f64(loss), want_loss, np.abs(want_loss) * 2.0 ** -20 + 1e-4, "loss")
         ops._assert_within(ops._f64(lse), want_lse, np.abs(want_lse) * 2.0 ** -22, "lse")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(5, 64), (640, 64), (640, 2048)])
+@pytest.mark.parametrize("shift", [0.0, 56.0, -56.0, 3.0e4])
+def test_distill_small_loss_does_not_depend_on_a_shift(dtype, T, V, shift):
+    # a student that equals its teacher: loss 0, and a gradient of 0, whatever is added to all of its logits
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    if dtype == "bf16" and abs(shift) > 56.0:
+        pytest.skip("the shifted logits are no bf16 values")
+    top = min(V, 512)
+    rng = np.random.default_rng(71)
+    teacher = (rng.integers(-32, 32, (T, top)) / 4.0).astype(np.float32)   # steps of 1/4: exact in bf16 below 64
+    index = np.stack([rng.permutation(V)[:top] for _ in range(T)]).astype(np.int32)
+    z = np.full((T, V), -np.inf)
+    np.put_along_axis(z, index.astype(np.int64), teacher + shift, 1)
+    zd = torch.from_numpy(z).to(ops._dt(dtype)).cuda()
+    assert (ops._f64(zd) == z).all()
+    loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), ops._dt(dtype))
+    mb.distill_loss(zd, ops._code(dtype), T, V, V, to_dev(teacher), to_dev(index), top, 1.0, None, loss, lse, dz, V)
+    torch.cuda.synchronize()
+    t64 = teacher.astype(np.float64)
+    gap = t64 - t64.max(1, keepdims=True)
+    p = np.exp(gap) / np.exp(gap).sum(1, keepdims=True)
+    # per entry: the teacher's and the student's exponents are off by 2^-24 of |gap| + 1 each and their factors by as
+    # much; the logarithms of the two sums, of their exponentials' 2^-22 and of their own 2^-23 each
+    tol = (8 + 4 * (p * np.abs(gap)).sum(1)) * 2.0 ** -23
+    ops._assert_within(ops._f64(loss), np.zeros(T), tol, "loss")
+    q = np.zeros((T, V))
+    np.put_along_axis(q, index.astype(np.int64), p, 1)
+    ops._assert_within(ops._f64(dz), np.zeros((T, V)), q * 2.0 ** -18 + 1e-38, "dz")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [515, 2053, 9001])
+def test_distill_many_rows_with_peaks_and_holes(dtype, V):
+    # single logits far above all others (a row's first reference is far below its sum, or as far as it may be), rows
+    # with few logits left, and rows with one
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, top, tau = 640, 7, 1.0
+    z, teacher, index, weight, _ = ops._distill_case(T, V, top, 81, dtype, masked=False)
+    rng = np.random.default_rng(82)
+    for t in range(T):
+        kind = t % 4
+        if kind < 2:
+            z[t, rng.integers(0, V)] = (18.0, 24.0, 45.0, 90.0)[t // 4 % 4]
+            z[t, index[t, 2]] += (15.0, 40.0)[kind]
+        else:
+            keep = index[t].astype(np.int64) if kind == 2 else index[t, :1].astype(np.int64)
+            row = torch.full((V,), float("-inf") if t % 8 < 4 else -1e9, dtype=z.dtype)
+            row[keep] = z[t, keep] + (0.0, -700.0, 900.0)[t // 4 % 3]
+            z[t] = row
+            if kind == 3:
+                index[t, 1:] = -1
+    loss, lse, dz = guarded((T,), torch.float32), guarded((T,), torch.float32), guarded((T, V), ops._dt(dtype))
+    mb.distill_loss(z.cuda(), ops._code(dtype), T, V, V, to_dev(teacher), to_dev(index), top, tau, to_dev(weight), loss,
+                    lse, dz, V)
+    torch.cuda.synchronize()
+    assert mb.read_device_errors() == 0
+    clean = torch.where(z == torch.tensor(-1e9).to(z.dtype), torch.full_like(z, float("-inf")), z)
+    # Here q passes through 2^-126, below which the kernels' exponential is 0: q is then off by up to that and dz by
+    # weight / tau of it, 1.5 x 2^-126 = 1.8e-38, which _check_distill (1e-38) does not hold.  Such values are looked
+    # at here and handed on as the formula's.
+    got = ops._f64(dz)
+    z64 = clean.double().numpy()
+    ones = np.ones(T)
+    _, _, want, q, p = F.distill(z64, teacher.astype(np.float64), index, tau, weight.astype(np.float64), ones)
+    flushed = (q < 2.0 ** -125) & (p == 0)
+    ops._assert_within(got[flushed], want[flushed], weight.max() / tau * 2.0 ** -126 * (1 + 2.0 ** -8), "flushed")
+    ops._check_distill(clean, teacher, index, weight, np.ones(T, dtype=np.float32), tau, V, dtype, ops._f64(loss),
+                       ops._f64(lse), np.where(flushed, want, got))
