@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
     return static_cast<const void*>(static_cast<const char*>(p.z) + t * p.ld * D::kBytes);
   };
   auto grads_of = [&](size_t t) { return static_cast<void*>(static_cast<char*>(p.dz) + t * p.ld_dz * D::kBytes); };
-  auto weight_of = [&](size_t t) { return p.weight != nullptr ? __ldg(p.weight + t) : 1.f; };
+  auto weight_of = [&](size_t t) { return p.weight != nullptr ? p.weight[t] : 1.f; };
   auto list_of = [&](int i) { return teacher_at(lists + i % kRingLists * tbytes, p.top); };
   bool ok = true;
   auto failed = [&]() {

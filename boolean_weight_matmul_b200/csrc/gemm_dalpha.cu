@@ -257,8 +257,8 @@ gemm_dalpha_kernel(const __grid_constant__ DaMaps maps, const __grid_constant__ 
           const uint8_t* src = m.packed + (size_t(r >> 3) * m.K + k) * p.N + size_t(g) * 128 + 2 * (r & 7);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            w[c][k] = uint32_t(__ldg(reinterpret_cast<const uint16_t*>(src + 32 * c))) |
-                      (uint32_t(__ldg(reinterpret_cast<const uint16_t*>(src + 32 * c + 16))) << 16);
+            w[c][k] = uint32_t(*reinterpret_cast<const uint16_t*>(src + 32 * c)) |
+                      (uint32_t(*reinterpret_cast<const uint16_t*>(src + 32 * c + 16)) << 16);
         }
       }
       float S[MBOK_MAX_K] = {0.f, 0.f, 0.f, 0.f};

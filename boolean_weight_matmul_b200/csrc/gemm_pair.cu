@@ -352,7 +352,7 @@ __device__ __forceinline__ void pair_drain(const PairParams& p, uint32_t tmem, c
     float v[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 s = __ldg(reinterpret_cast<const float4*>(p.inverse + t) + i);
+      const float4 s = *(reinterpret_cast<const float4*>(p.inverse + t) + i);
       v[4 * i] = __uint_as_float(w[4 * i]) * s.x;
       v[4 * i + 1] = __uint_as_float(w[4 * i + 1]) * s.y;
       v[4 * i + 2] = __uint_as_float(w[4 * i + 2]) * s.z;

@@ -215,7 +215,7 @@ __device__ __forceinline__ void load_b(const GemvMmaParams& p, int n, int q, uin
   }
   if (!XF32) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x) + size_t(vec) * p.s.N + q * kUnit);
-    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+    const uint4 v0 = src[0], v1 = src[1];
     b[0] = v0.x; b[1] = v0.y; b[2] = v0.z; b[3] = v0.w;
     b[4] = v1.x; b[5] = v1.y; b[6] = v1.z; b[7] = v1.w;
   } else {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void load_b(const GemvMmaParams& p, int n, int q, uin
     const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + size_t(vec) * p.s.N + q * kUnit);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(src + i);
+      const float4 v = src[i];
       b[2 * i] = bf16_part(v.x, part) | (bf16_part(v.y, part) << 16);
       b[2 * i + 1] = bf16_part(v.z, part) | (bf16_part(v.w, part) << 16);
     }

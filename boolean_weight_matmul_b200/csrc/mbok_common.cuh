@@ -67,7 +67,9 @@ __device__ __forceinline__ void store_act(void* out, bool bf16, size_t i, float 
 }
 
 // Programmatic dependent launch: return once the preceding grid of the stream is
-// complete; let the following grid start.
+// complete; let the following grid start.  What the preceding grid may write is
+// written while this one already runs, so that it is read by ordinary loads behind
+// the wait, never through the read-only path (__ldg).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 

@@ -20,7 +20,7 @@ constexpr int kScaleThreads = 256;
 // before; the row's last value, which may be the tensor's, is read alone).  1700
 // tokens of two dY, 287 and 9553 rows: 28 us by single values, 22 by words.
 __device__ __forceinline__ uint4 row_vec(const uint16_t* row, int cols, int v, bool vectors) {
-  if (vectors) return __ldg(reinterpret_cast<const uint4*>(row) + v);
+  if (vectors) return *(reinterpret_cast<const uint4*>(row) + v);
   const int odd = int(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
   uint32_t w[5];
 #pragma unroll
@@ -28,7 +28,7 @@ __device__ __forceinline__ uint4 row_vec(const uint16_t* row, int cols, int v, b
     const int c = 8 * v + 2 * i - odd;   // the word's first value
     w[i] = 0u;
     if (i < 4 || odd) {
-      if (c + 1 < cols) w[i] = __ldg(reinterpret_cast<const uint32_t*>(row + c));
+      if (c + 1 < cols) w[i] = *reinterpret_cast<const uint32_t*>(row + c);
       else if (c < cols) w[i] = row[c];
     }
   }
