@@ -104,7 +104,8 @@ def _marshal():
     18.5 -> 10.0 us, gemv_gated 10.5 -> 6.2 us."""
     global _marshal_module
     if _marshal_module is None:
-        path = os.path.join(_HERE, "_marshal.so")
+        from .build import marshal_path
+        path = marshal_path()
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing; build it with `python -m boolean_weight_matmul_b200.build`")
         spec = importlib.util.spec_from_file_location(__name__ + "._marshal", path)

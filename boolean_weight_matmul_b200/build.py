@@ -10,7 +10,8 @@ the same sources with MBOK_PHASE_STAMPS defined: the decode lookup kernels
 then record per-CTA phase timestamps (read by `bench.py --phase-profile`).
 
 csrc/marshal.cpp, the binding's argument marshalling, becomes the extension
-module boolean_weight_matmul_b200/_marshal.so (C++, against torch's headers).
+module boolean_weight_matmul_b200/_marshal.<Python ABI>.torch-<version>.so (C++,
+against torch's headers, so that each pair of versions has its own).
 """
 from __future__ import annotations
 
@@ -29,7 +30,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmbok.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
-MARSHAL = os.path.join(HERE, "_marshal.so")
 VARIANTS = {"": ("libmbok.so", []), "stamps": ("libmbok_stamps.so", ["-DMBOK_PHASE_STAMPS"])}
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -71,15 +71,23 @@ def _compile(src: str, verbose: bool, out_dir: str = BUILD_DIR, extra=()) -> str
     return obj
 
 
+def marshal_path() -> str:
+    """The extension module of this Python and this torch, whose ABIs it is
+    compiled for."""
+    import torch
+    return os.path.join(HERE, f"_marshal.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
 def build_marshal(force: bool = False) -> str:
-    """Compile the extension module _marshal.so; returns its path."""
+    """Compile the extension module; returns its path."""
+    path = marshal_path()
     deps = [MARSHAL_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in deps):
-        return MARSHAL
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
-    tmp = MARSHAL + ".tmp"
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"]]
@@ -91,8 +99,8 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, variant: str = "") -> str:

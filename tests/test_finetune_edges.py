@@ -180,15 +180,13 @@ def test_distill_huge_logits(T):
         ops._assert_within(ops._f64(lse), want_lse, np.abs(want_lse) * 2.0 ** -22, "lse")
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,V", [(5, 64), (640, 64), (640, 2048)])
-@pytest.mark.parametrize("shift", [0.0, 56.0, -56.0, 3.0e4])
+@pytest.mark.parametrize("dtype,shift", [("f32", 0.0), ("bf16", 0.0), ("f32", 56.0), ("bf16", 56.0), ("f32", -56.0),
+                                         ("bf16", -56.0), ("f32", 3.0e4)])   # 3e4 + 1/4 is no bf16 value
 def test_distill_small_loss_does_not_depend_on_a_shift(dtype, T, V, shift):
     # a student that equals its teacher: loss 0, and a gradient of 0, whatever is added to all of its logits
     import torch
     import boolean_weight_matmul_b200 as mb
-    if dtype == "bf16" and abs(shift) > 56.0:
-        pytest.skip("the shifted logits are no bf16 values")
     top = min(V, 512)
     rng = np.random.default_rng(71)
     teacher = (rng.integers(-32, 32, (T, top)) / 4.0).astype(np.float32)   # steps of 1/4: exact in bf16 below 64
