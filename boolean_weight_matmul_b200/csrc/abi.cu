@@ -444,11 +444,16 @@ int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* 
   if (any && overlap(dX, x_bytes, X, x_bytes)) return MBOK_ERR_INVALID_ARG;
   for (int i = 0; i < nseg; ++i)
     if (any && overlap(dX, x_bytes, dY[i], size_t(T) * M[i] * 2)) return MBOK_ERR_INVALID_ARG;
-  // a matrix given twice has two gradients: they are not added up
-  for (int i = 0; any && i < nseg; ++i)
-    for (int j = 0; j < i; ++j)
-      if (overlap(dalpha[i], mbok_alpha_elems(K[i], M[i], N) * 4, dalpha[j], mbok_alpha_elems(K[j], M[j], N) * 4))
+  // and are written while those are read; a matrix given twice has two gradients:
+  // they are not added up
+  for (int i = 0; any && i < nseg; ++i) {
+    const size_t bytes = mbok_alpha_elems(K[i], M[i], N) * 4;
+    if (overlap(dalpha[i], bytes, dX, x_bytes) || overlap(dalpha[i], bytes, X, x_bytes)) return MBOK_ERR_INVALID_ARG;
+    for (int j = 0; j < nseg; ++j)
+      if (overlap(dalpha[i], bytes, dY[j], size_t(T) * M[j] * 2) ||
+          (j < i && overlap(dalpha[i], bytes, dalpha[j], mbok_alpha_elems(K[j], M[j], N) * 4)))
         return MBOK_ERR_INVALID_ARG;
+  }
   return from_cuda(launch_gemm_backward(nseg, p8, alpha, shapes, X, T, dY, dX, dalpha, workspace, as_stream(stream)));
 }
 

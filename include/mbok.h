@@ -340,8 +340,8 @@ size_t mbok_gemm_backward_workspace_bytes(int nseg, const int* K, const int* M, 
  *            (mbok_alpha_elems(K[s], M[s], N) elements, pad rows 0), or NULL;
  *            an entry may be NULL (a matrix whose scales are frozen).
  *   All 16-byte aligned; 1 <= T <= 2^23.  With dalpha asked for, dX must not
- *   overlap X or a dY, nor one dalpha another, also where a matrix is given
- *   twice (MBOK_ERR_INVALID_ARG).
+ *   overlap X or a dY, nor a dalpha any of these, dX or another dalpha, also where
+ *   a matrix is given twice (MBOK_ERR_INVALID_ARG).
  * dX: dY scaled to fp16 per token (over all matrices), weight levels rounded
  * once to fp16, as mbok_gemm_gated; one fp32 sum over all matrices, rounded
  * once.  dalpha: products of the bf16 values are exact, sums fp32; the dense

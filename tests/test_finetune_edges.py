@@ -249,3 +249,34 @@ def test_distill_many_rows_with_peaks_and_holes(dtype, V):
     ops._assert_within(got[flushed], want[flushed], weight.max() / tau * 2.0 ** -126 * (1 + 2.0 ** -8), "flushed")
     ops._check_distill(clean, teacher, index, weight, np.ones(T, dtype=np.float32), tau, V, dtype, ops._f64(loss),
                        ops._f64(lse), np.where(flushed, want, got))
+
+
+# ---- outputs over inputs, where that is allowed ----------------------------------------
+
+def test_token_products_over_their_inputs():
+    # the gated product over X, dX over X's place or a dY (without scale gradients): the bits of separate buffers, whole
+    # tiles and cut ones
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    for N, T in ((256, 77), (2304, 40), (1280, 600)):
+        gate, up = ops.Layer(2, N, N, 301), ops.Layer(3, N, N, 302)
+        X = ops.x_dev(ops.wl.x_normal(T, N, 303), "bf16")
+        for keep in (False, True):
+            want = ops._gemm_gated(gate, up, X, keep)
+            ws = mb.empty_gemm_gated_workspace(N, N, T)
+            outs = [X.clone(), torch.zeros_like(X), torch.zeros_like(X)]
+            mb.gemm_gated(gate.packed, gate.blocked, 2, up.packed, up.blocked, 3, N, N, 128, outs[0], T, outs[0],
+                          outs[1] if keep else None, outs[2] if keep else None, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], want[0])
+            assert not keep or (torch.equal(outs[1], want[1]) and torch.equal(outs[2], want[2]))
+        dYs = [ops._grads(T, N, 304), ops._grads(T, N, 305)]
+        want, _ = ops._gemm_backward([gate, up], X, dYs, want_a=[False, False])
+        ws = mb.empty_gemm_backward_workspace([2, 3], [N, N], N, T)
+        for over in (0, 1):
+            d = [t.clone() for t in dYs]
+            mb.gemm_backward([gate.packed, up.packed], [gate.blocked, up.blocked], [2, 3], [N, N], N, 128, None, T, d,
+                             d[over], None, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(d[over], want) and torch.equal(d[1 - over], dYs[1 - over])
+        assert mb.read_device_errors() == 0
