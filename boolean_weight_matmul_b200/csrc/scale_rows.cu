@@ -2,8 +2,8 @@
 // times a power of two that puts its largest finite magnitude in [2^14, 2^15).
 //
 // fp16 holds 11 bits where bf16 holds 8, so the scaled values are exact down
-// to 2^-29 of the token's largest and off by at most 2^-40 of it below that,
-// far under the fp32 accumulation; and weight levels, which need more than
+// to 2^-29 of the token's largest and off by at most 2^-39 of it below that (half
+// a step of fp16's subnormals, 2^-25, where the largest is 2^14), far under the fp32 accumulation; and weight levels, which need more than
 // bf16's 8 bits, keep 11 in the same tensor-core instruction.  (An instruction
 // takes two operands of one type; bf16 levels would add an error as large as
 // the output's own rounding, and two bf16 terms per level twice the work.)

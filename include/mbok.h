@@ -314,7 +314,7 @@ size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T);
  *   another (MBOK_ERR_INVALID_ARG).  Other arguments as mbok_gemv_gated.
  *   workspace: mbok_gemm_gated_workspace_bytes(M, N, T) bytes.
  * Each token's X is scaled by a power of two into fp16 (exact, but for values
- * below 2^-29 of the token's largest, which are off by at most 2^-40 of it),
+ * below 2^-29 of the token's largest, which are off by at most 2^-39 of it),
  * each weight level rounded once to fp16 (relative 2^-11 for levels above
  * 2^-12, absolute 2^-23 below), accumulation fp32, H computed from the fp32 G
  * and U, every output rounded once: deterministic.  Waits inside the kernel

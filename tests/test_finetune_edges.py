@@ -280,3 +280,31 @@ def test_token_products_over_their_inputs():
             torch.cuda.synchronize()
             assert torch.equal(d[over], want) and torch.equal(d[1 - over], dYs[1 - over])
         assert mb.read_device_errors() == 0
+
+
+# ---- scaled activations ------------------------------------------------------------------
+
+def test_gemm_gated_smallest_activations_beside_a_large_one():
+    # Each token's values are scaled so that its largest lies in [2^14, 2^15), and rounded to fp16, whose subnormals are
+    # 2^-24 apart: off by at most 2^-25, that is 2^-39 of a largest value of 1.  The first group's scales are 0, so
+    # that only the small values reach the result.
+    import torch
+    M, N, T = 16, 256, 8
+    gate, up = ops.Layer(1, M, N, 401), ops.Layer(1, M, N, 402)
+    x = np.zeros((T, N))
+    x[:, 0] = 1.0
+    for t in range(T):
+        x[t, 128:] = np.where(np.arange(128) % (t + 1) == 0, (1.5, 1.25, 3.5, 0.75)[t % 4], 0.0) * 2.0 ** -38
+    X = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    assert (ops._f64(X) == x).all()
+    for layer in (gate, up):
+        blocked = layer.blocked.view(-1, N // 128, 1, 8)
+        blocked[:, 0] = 0.0
+        blocked[:, 1] = 1.0
+        layer.alpha = layer.alpha.copy()
+        layer.alpha[:, 0], layer.alpha[:, 1] = 0.0, 1.0
+    got = ops._gemm_gated(gate, up, X, True)
+    for layer, out in ((gate, got[1]), (up, got[2])):
+        want = x @ ops._dense_abs(layer).T
+        tol = 2.0 ** -39 * (x[:, 128:] != 0).sum(1, keepdims=True) + np.abs(want) * ops.HALF["bf16"]
+        ops._assert_within(ops._f64(out), want, tol)
