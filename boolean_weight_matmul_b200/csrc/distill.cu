@@ -796,7 +796,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
 
   if (warp < kRingRowWarps) {
     // ---- the rows (a wait that gave up is not waited for again, but the warps
-    // keep to their barriers) ----
+    // keep to their barriers; what they still write stays within the outputs, which
+    // are undefined then) ----
     const int gt = threadIdx.x;
     float w = weight_of(row_of(0));
     for (int i = 0; i < nrows; ++i) {

@@ -479,9 +479,9 @@ int mbok_gemv_noalloc(const uint32_t* packed, const uint16_t* alpha, int K, int 
  * which case that CTA stored none of its rows of y; bit 1 = a prefill-GEMM
  * pipeline wait gave up; bit 2 = a tensor-core GEMV copy wait gave up, bit 3 = a
  * CTA-pair GEMM (mbok_gemm_gated, mbok_gemm_backward) pipeline wait gave up,
- * bit 4 = a copy wait of mbok_distill_loss gave up, in
- * which case that launch stored no outputs) and clears them.  Synchronises
- * the device.  Returns MBOK_ERR_CUDA if the flags cannot be read. */
+ * bit 4 = a copy wait of mbok_distill_loss gave up; after bits 1 to 4 that
+ * launch's outputs are undefined, some of them stored) and clears them.
+ * Synchronises the device.  Returns MBOK_ERR_CUDA if the flags cannot be read. */
 int mbok_read_device_errors(unsigned* flags);
 
 /* Self-check of the bounded waits that the pipelined kernels use: launches
