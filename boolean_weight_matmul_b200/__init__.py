@@ -310,10 +310,6 @@ def gemv_svid(packed, s_in, s_out, K, M, N, x, x_dtype, batch, y, workspace, str
            "mbok_gemv_svid")
 
 
-def _ws_bytes(workspace) -> int:
-    return workspace.numel() * workspace.element_size() if workspace is not None else 0
-
-
 def gemv_gated_workspace_bytes(K_gate: int, K_up: int, M: int, N: int, batch: int = 1) -> int:
     return int(lib().mbok_gemv_gated_workspace_bytes(K_gate, K_up, M, N, batch))
 

@@ -61,7 +61,7 @@ struct DaMaps {
 struct DaParams {
   DaMat mat[kMaxMats];
   int nmat;
-  int N, G, T;
+  int N, G;
   int col_tiles;        // of 256 columns
   int ntiles;           // over all matrices
   int splits;
@@ -401,7 +401,6 @@ cudaError_t launch_gemm_dalpha(int nmat, const uint8_t* const* packed, const Sha
   p.nmat = nmat;
   p.N = shapes[0].N;
   p.G = shapes[0].G;
-  p.T = T;
   p.col_tiles = (p.N + 255) / 256;
   p.stages = (T + kDaBT - 1) / kDaBT;
   p.splits = splits;
