@@ -535,7 +535,7 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
   }
   // The next grid may start from here on: started with this one, its CTAs filled
   // the SMs unevenly where a grid is less than a wave (82 x 5591 fp32: 7.6 us, from
-  // here 5.3; 64 x 128000 bf16 13.9 and 13.3).
+  // here 5.5; 64 x 128000 bf16 4 % less).
   pdl_launch();
   const bool used = w != 0.f && teach.some() != 0;
   if (!used) {
@@ -645,7 +645,7 @@ distill_grad_kernel(const __grid_constant__ DistillParams p) {
 // maximum, exponents of rows at 69 were off by 2^-18 and losses by 4e-6.)
 // Only the last step needs the list: it is long in coming for the first row.
 // 2048 x 32000 bf16, loss and gradient: 59.5 us, 4.4 TB/s of logits and gradients
-// (two passes on independent CTAs: 74 us).  The exponentials' pipe is 53 % busy, the
+// (two passes on independent CTAs: 74 us).  The exponentials' pipe is 52 % busy, the
 // issue slots 65 %: a row's two passes and their barriers take as long as its copies.
 //
 // In place: a slot is copied out behind its list (done), and a row's ends, which no

@@ -48,11 +48,13 @@
 // flag, drains what it issued (bounded) and leaves with the other.
 //
 // Measured (LLaMA-7B gate and up, K = 3, 4096 columns, with the scaling pass):
-//   GATE  2048 tokens 285 us = 1295 TFLOP/s (a plain bf16 GEMM of the library
-//         under the same load, which the power limit sets: 1354); tensor pipe
-//         64 % and ALU pipe 72 % busy.  K = 4: 366 to 375 us, bound by the unpack.
+//   GATE  2048 tokens 286 us = 1291 TFLOP/s in short runs, 332 us = 1112 under the
+//         power limit of long ones (a plain bf16 GEMM of the library: 1632 and
+//         1354); tensor pipe 64 % and ALU pipe 72 % busy.  K = 4: 366 to 375 us,
+//         bound by the unpack.
 //   GATE  256 tokens 62 us, 32 tokens 39 us (81 and 50 at the clocks that calls of
-//         2048 tokens leave): the unpack and the pipeline's fill.
+//         2048 tokens leave): the latency of a stage's unpack (32 tokens: ALU 63 %,
+//         issue 58 %) and the pipeline's fill.
 //   GRAD  2048 tokens 280 .. 300 us, 256 tokens 76 us.
 #include "pair_ring.h"
 #include "scale_rows.h"

@@ -45,7 +45,8 @@
 // Measured in a graph: LLaMA-7B gate and up (K = 3) 27.1 us for 2 to 8 vectors,
 // 41.1 us for 16; LLaMA-13B (K = 4 and 2, 5120 columns) 38.9 us for 7, of which 17 us
 // are the MMAs and their ANDs (each about 8 cycles of its pipe per MMA), 3.6 us
-// the copies' instructions, 3.6 us the joined sums.
+// the copies' instructions, 3.6 us the joined sums.  All forms spill registers (44 to
+// 244 bytes of stores a thread, 92 to 352 of loads).
 #include "lut_common.cuh"
 #include "tc_common.cuh"
 

@@ -317,8 +317,8 @@ size_t mbok_gemm_gated_workspace_bytes(int M, int N, int T);
  * below 2^-29 of the token's largest, which are off by at most 2^-39 of it),
  * each weight level rounded once to fp16 (relative 2^-11 for levels above
  * 2^-12, absolute 2^-23 below), accumulation fp32, H computed from the fp32 G
- * and U, every output rounded once: deterministic.  Waits inside the kernel
- * are bounded: see mbok_read_device_errors (bit 3). */
+ * and U (a sigmoid below 2^-126 as 0), every output rounded once: deterministic.
+ * Waits inside the kernel are bounded: see mbok_read_device_errors (bit 3). */
 int mbok_gemm_gated(const uint32_t* packed_gate, const uint16_t* alpha_gate, int K_gate, const uint32_t* packed_up,
                     const uint16_t* alpha_up, int K_up, int M, int N, int group, const uint16_t* X, int T, uint16_t* H,
                     uint16_t* gate, uint16_t* up, void* workspace, size_t workspace_bytes, void* stream);
@@ -362,7 +362,8 @@ int mbok_gemm_backward(int nseg, const uint32_t* const* packed, const uint16_t* 
  *                     output may be one of the inputs (the same address) and
  *                     must not overlap another array otherwise
  *                     (MBOK_ERR_INVALID_ARG).
- * All 16-byte aligned.  1 <= T <= 2^23, 1 <= M <= 2^22. */
+ * All 16-byte aligned.  1 <= T <= 2^23, 1 <= M <= 2^22.  Computed in fp32; a
+ * sigmoid below 2^-126 (g below -87) may come out as 0. */
 int mbok_gated_backward(const uint16_t* dH, const uint16_t* gate, const uint16_t* up, int T, int M, uint16_t* dgate,
                         uint16_t* dup, uint16_t* H, void* stream);
 
@@ -400,7 +401,8 @@ int mbok_distill_loss(const void* logits, int dtype, int T, int V, size_t ld, co
 /* The gradient alone, from the lse that mbok_distill_loss returned for the
  * same arguments and the gradient of the loss that followed:
  *     dlogits[t][j] = grad[t] weight[t] / tau (q_j - sum of p_i with index[t][i] = j),
- * q_j = exp(logits[t][j] / tau - lse[t]).  grad: fp32 [T], or NULL for 1 (of a
+ * q_j = exp(logits[t][j] / tau - lse[t]), so that q carries lse's rounding to
+ * fp32 (2^-24 of lse, relative to q).  grad: fp32 [T], or NULL for 1 (of a
  * token of weight 0 or with nothing listed it may be anything).
  * Other arguments as mbok_distill_loss. */
 int mbok_distill_backward(const void* logits, int dtype, int T, int V, size_t ld, const float* teacher,
