@@ -465,10 +465,11 @@ __global__ void __launch_bounds__(256) gemv_gated_combine_kernel(const float* __
 // Chunks of vectors (one takes two 8-column tiles at most), as equal as can be, and
 // the fragment columns of one.  Chunks run side by side in one launch: their CTAs
 // share the weights through L2, and few rows leave SMs for all (one launch after
-// another against side by side, fp32: 11 vectors, 70 rows, N = 1664 38 -> 15 us; 16
-// vectors, LLaMA-7B gate and up 166 -> 146 us; 6 vectors there 76 -> 80: two chunks
-// alone lose a little).  Each chunk streams all weights, so that the time steps with
-// their number: LLaMA-7B, fp32, 3 to 5 vectors 44 us, 6 to 10 80, 11 to 15 115, 16 145.
+// another against side by side, fp32, equal chunks: 6 vectors, 70 rows, N = 1664 31
+// and 16 us; LLaMA-7B gate and up, 6 vectors 87 and 80, 16 vectors 175 and 145; 5 and
+// 1 vectors one after another, the last on one tile, 76).  Each chunk streams all
+// weights, so that the time steps with their number: LLaMA-7B, fp32, 3 to 5 vectors
+// 44 us, 6 to 10 80, 11 to 15 115, 16 145.
 static int gd_chunks(bool x_f32, int batch) { return x_f32 ? (batch + 4) / 5 : (batch + 15) / 16; }
 static int gd_columns(bool x_f32, int nb) { return x_f32 ? 3 * nb : nb; }
 
