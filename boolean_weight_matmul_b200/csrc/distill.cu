@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) distill_ring_kernel(const __g
   __shared__ __align__(16) float warp_val[3][kRingRowWarps];
   __shared__ float row_from[kRingSlots];                 // the first sum's reference
   __shared__ float4 row_sum[kRingSlots];                 // reference, sum, weight, whether summed from the maximum
-  __shared__ int s_fail;                                 // a wait gave up: nothing more is stored
+  __shared__ int s_fail;                                 // a wait gave up: no row is copied out any more
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tbytes = teacher_bytes(p.top);
   unsigned char* lists = ring + kRingSlots * rp.slot_bytes;

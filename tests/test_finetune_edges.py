@@ -308,3 +308,41 @@ def test_gemm_gated_smallest_activations_beside_a_large_one():
         want = x @ ops._dense_abs(layer).T
         tol = 2.0 ** -39 * (x[:, 128:] != 0).sum(1, keepdims=True) + np.abs(want) * ops.HALF["bf16"]
         ops._assert_within(ops._f64(out), want, tol)
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 1003), ("f32", 1000)])
+def test_distill_many_rows_without_a_distribution(dtype, V):
+    # rows with a NaN, with +infinity, with nothing but masks, unused ones among them: NaN and 0 stay in their rows
+    import torch
+    import boolean_weight_matmul_b200 as mb
+    T, top, tau = 640, 6, 2.0
+    z, teacher, index, weight, _ = ops._distill_case(T, V, top, 91, dtype, masked=False)
+    clean = z.clone()
+    for t in range(0, T, 5):
+        kind = t // 5 % 6
+        if kind < 3:
+            z[t, (0, V // 2, V - 1)[kind]] = float("nan")
+        elif kind == 3:
+            z[t, V - 2] = float("inf")
+        else:
+            z[t] = float("-inf") if kind == 4 else torch.finfo(z.dtype).min
+    index[7::25] = -1
+    weight[10::25] = 0.0
+    bad = np.zeros(T, dtype=bool)
+    bad[::5] = True
+    unused = (weight == 0) | (index < 0).all(1)
+    args = (ops._code(dtype), T, V, V, to_dev(teacher), to_dev(index), top, tau, to_dev(weight))
+    ones = np.ones(T, dtype=np.float32)
+    for place in ("own", "over the logits"):
+        zd = z.cuda()
+        loss, lse = guarded((T,), torch.float32), guarded((T,), torch.float32)
+        dz = guarded((T, V), ops._dt(dtype)) if place == "own" else zd
+        mb.distill_loss(zd, *args, loss, lse, dz, V)
+        torch.cuda.synchronize()
+        assert mb.read_device_errors() == 0
+        got = ops._f64(dz)
+        assert np.isnan(ops._f64(loss)[bad & ~unused]).all() and np.isnan(got[bad & ~unused]).all()
+        assert (ops._f64(loss)[unused] == 0).all() and (got[unused] == 0).all()
+        good = ~bad
+        ops._check_distill(clean[good], teacher[good], index[good], weight[good], ones[good], tau, V, dtype,
+                           ops._f64(loss)[good], ops._f64(lse)[good], got[good])
